@@ -206,6 +206,63 @@ PLORA_API plora_status plora_backward(plora_handle h, const void* X, const void*
                             const plora_adapter* tab, const void* saved, void* stream);
 
 /*
+ * The projection with its epilogue: bias, activation and residual, forward and backward.
+ *
+ *     Z_i  = X_i W + s_i (X_i A_i) B_i + b_i         Y = act(Z) + R
+ *     dZ   = dY * act'(Z)       db_i = sum of dZ over adapter i's rows       dR = dY
+ * and dX, dA_i, dB_i as for plora_backward with dZ in the place of dY.
+ *
+ * b_i is the projection's bias (PEFT trains one per adapter with bias="lora_only"; a frozen bias that
+ * every adapter shares is the same pointer for each).  It is added to the fp32 sum, and so are the
+ * activation and the residual: Y and Z are each rounded once.
+ *
+ * Supported by fp32 handles and by bf16 handles on the default tensor-core path (output blocks too);
+ * PLORA_FLAG_SIMT on a bf16 handle, PLORA_FLAG_UNFUSED and PLORA_FLAG_BASE_PAIR return
+ * PLORA_ERR_UNSUPPORTED.
+ */
+typedef enum {
+    PLORA_ACT_NONE = 0,
+    PLORA_ACT_RELU = 1,       /* derivative 0 at 0 */
+    PLORA_ACT_GELU = 2,       /* z (1 + erf(z / sqrt 2)) / 2 */
+    PLORA_ACT_GELU_TANH = 3,  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+    PLORA_ACT_SILU = 4        /* z / (1 + exp(-z)) */
+} plora_activation;
+
+/*
+ * activation: a plora_activation; reserved: 0.  bias, dbias: HOST arrays of n_adapters device pointers,
+ * or NULL; an entry may be NULL (no bias, no gradient wanted).  bias[i]: [d_out] in the handle's dtype;
+ * dbias[i]: [d_out] fp32, overwritten (zero for an adapter without tokens).  residual: [T][d_out] in the
+ * handle's dtype or NULL; with a bf16 handle it may be Y itself (added in place).  Z: [T][d_out] in the handle's dtype:
+ * written by the forward (NULL: not kept), read by the backward of an activation.  work: the backward's
+ * scratch, plora_epilogue_work_bytes() bytes, 256-byte aligned (may be NULL if that is 0).  The forward
+ * ignores dbias and work, the backward bias and residual (dR is dY).  Every other pointer is 16-byte
+ * aligned.  A buffer that a call writes must not overlap another of these buffers, Y, dY or dX
+ * (PLORA_ERR_INVALID_ARG), except residual = Y.
+ */
+typedef struct {
+    int32_t activation;
+    int32_t reserved;
+    const void* const* bias;
+    float* const* dbias;
+    const void* residual;
+    void* Z;
+    void* work;
+} plora_epilogue;
+
+/* Size of the backward's scratch for this segment map, activation and set of wanted dbias entries. */
+PLORA_API plora_status plora_epilogue_work_bytes(plora_handle h, int32_t n_adapters, const int64_t* off,
+                                                 const plora_epilogue* ep, size_t* bytes);
+/* plora_forward with an epilogue (not NULL).  Other arguments, errors and captures as for plora_forward. */
+PLORA_API plora_status plora_forward_epilogue(plora_handle h, const void* X, const void* W, void* Y,
+                                              int32_t n_adapters, const int64_t* off, const plora_adapter* tab,
+                                              void* saved, const plora_epilogue* ep, void* stream);
+/* plora_backward of a plora_forward_epilogue call.  dX may be NULL. */
+PLORA_API plora_status plora_backward_epilogue(plora_handle h, const void* X, const void* W, const void* dY,
+                                               void* dX, int32_t n_adapters, const int64_t* off,
+                                               const plora_adapter* tab, const void* saved,
+                                               const plora_epilogue* ep, void* stream);
+
+/*
  * Synchronise `stream` and report the handle's device error flag: PLORA_OK,
  * PLORA_ERR_TIMEOUT (a bounded device wait ran out), PLORA_ERR_BOUNDS (a
  * PLORA_DEBUG build's bounds check failed) or PLORA_ERR_CUDA.  A reported
@@ -289,6 +346,57 @@ typedef struct {
  */
 PLORA_API plora_status plora_adamw_step(plora_handle h, int32_t n_adapters, const plora_adapter* tab,
                                         const plora_adamw_state* st, void* stream);
+
+/*
+ * One Muon step for every adapter: momentum whose update is orthogonalised by Newton-Schulz products.
+ * Per matrix M -- A_i [r][d_in] and B_i [d_out][r]; with P output blocks each block's A_i [r][d_in] and
+ * B_i [width][r] are matrices of their own -- with g its gradient from the table:
+ *     m <- momentum m + g;     u = g + momentum m if nesterov, else m
+ *     X <- u / (|u|_F + eps);  ns_steps times X <- a X + (b X X^T + c (X X^T)^2) X
+ *     p <- p (1 - lr weight_decay) - lr k X
+ * with k = 1 (PLORA_MUON_SCALE_NONE), sqrt(max(1, rows / cols)) (_ROWS) or 0.2 sqrt(max(rows, cols))
+ * (_RMS); then the table's A_i / B_i receive p, rounded to nearest even for bf16.  The usual coefficients
+ * are a, b, c = 3.4445, -4.7750, 2.0315 with 5 steps.  X X^T is taken on the short side.  The Gram matrix
+ * and the iteration are in fp64, the rest in fp32.  A matrix whose u is all zero gets X = 0; one with a
+ * NaN or an infinity in u gets X = NaN throughout (other matrices are untouched by it).
+ * Adapters are independent, and a matrix's result does not depend on what else is packed with it.
+ */
+#define PLORA_MUON_MAX_STEPS 16
+typedef enum {
+    PLORA_MUON_SCALE_NONE = 0,
+    PLORA_MUON_SCALE_ROWS = 1,
+    PLORA_MUON_SCALE_RMS = 2
+} plora_muon_scale;
+
+/* Optimizer state of one adapter.  Arrays as for plora_adamw_state (fp32, shaped like the factors, 16-byte
+ * aligned, updated in place; the masters NULL with an fp32 handle). */
+typedef struct {
+    float lr;
+    float momentum;          /* in [0, 1) */
+    float weight_decay;      /* decoupled */
+    float eps;               /* > 0 */
+    float a, b, c;           /* finite */
+    int32_t ns_steps;        /* 1 .. PLORA_MUON_MAX_STEPS */
+    int32_t nesterov;        /* 0 or 1 */
+    int32_t scale;           /* a plora_muon_scale */
+    int32_t reserved;        /* 0 */
+    float* A_master;
+    float* B_master;
+    float* mA;
+    float* mB;
+} plora_muon_state;
+
+/* Size of the step's scratch for these adapters (their ranks alone are read). */
+PLORA_API plora_status plora_muon_work_bytes(plora_handle h, int32_t n_adapters, const plora_adapter* tab,
+                                             size_t* bytes);
+/*
+ * tab: host plora_adapter[n] (rank, A, B written, dA, dB read); st: host plora_muon_state[n]; work: device,
+ * 256-byte aligned, plora_muon_work_bytes() bytes, not shared with work that may run at the same time
+ * (another stream's step, a replayed graph).  No two written buffers, and no written and read one, may
+ * overlap.  Errors and captures as for plora_adamw_step.
+ */
+PLORA_API plora_status plora_muon_step(plora_handle h, int32_t n_adapters, const plora_adapter* tab,
+                                       const plora_muon_state* st, void* work, void* stream);
 
 /*
  * CUDA graph capture (a runtime facility; the pages describe no API).  A plora_forward,

@@ -40,6 +40,13 @@ PLORA_MAX_RANK = 256
 PLORA_MAX_ADAPTERS = 4096
 PLORA_MAX_OUT_BLOCKS = 8
 PLORA_STATIC_SCRATCH_BYTES = 16 << 20
+PLORA_ACT_NONE, PLORA_ACT_RELU, PLORA_ACT_GELU, PLORA_ACT_GELU_TANH, PLORA_ACT_SILU = range(5)
+PLORA_MUON_SCALE_NONE, PLORA_MUON_SCALE_ROWS, PLORA_MUON_SCALE_RMS = range(3)
+PLORA_MUON_MAX_STEPS = 16
+ACTIVATIONS = {"none": PLORA_ACT_NONE, "relu": PLORA_ACT_RELU, "gelu": PLORA_ACT_GELU,
+               "gelu_tanh": PLORA_ACT_GELU_TANH, "silu": PLORA_ACT_SILU}
+MUON_SCALES = {"none": PLORA_MUON_SCALE_NONE, "rows": PLORA_MUON_SCALE_ROWS, "rms": PLORA_MUON_SCALE_RMS}
+MUON_COEFFS = (3.4445, -4.7750, 2.0315)
 
 EXPORTED = ("plora_create", "plora_destroy", "plora_saved_bytes", "plora_forward", "plora_backward",
             "plora_check", "plora_status_string", "plora_last_error", "plora_debug_unpack_saved",
@@ -47,7 +54,9 @@ EXPORTED = ("plora_create", "plora_destroy", "plora_saved_bytes", "plora_forward
             "plora_grad_B_static", "plora_adamw_step", "plora_debug_timeout_probe", "plora_device_info",
             "plora_capture_reserve", "plora_capture_release", "plora_partition", "plora_debug_build",
             "plora_layer_create", "plora_layer_destroy", "plora_layer_handle", "plora_layer_saved_bytes",
-            "plora_layer_forward", "plora_layer_backward", "plora_layer_check", "plora_layer_last_error")
+            "plora_layer_forward", "plora_layer_backward", "plora_layer_check", "plora_layer_last_error",
+            "plora_epilogue_work_bytes", "plora_forward_epilogue", "plora_backward_epilogue",
+            "plora_muon_work_bytes", "plora_muon_step")
 
 
 class plora_config(ctypes.Structure):
@@ -80,6 +89,20 @@ class plora_adamw_state(ctypes.Structure):
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float), ("step", ctypes.c_int32),
                 ("A_master", ctypes.c_void_p), ("B_master", ctypes.c_void_p), ("mA", ctypes.c_void_p),
                 ("vA", ctypes.c_void_p), ("mB", ctypes.c_void_p), ("vB", ctypes.c_void_p)]
+
+
+class plora_epilogue(ctypes.Structure):
+    _fields_ = [("activation", ctypes.c_int32), ("reserved", ctypes.c_int32), ("bias", ctypes.c_void_p),
+                ("dbias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("Z", ctypes.c_void_p),
+                ("work", ctypes.c_void_p)]
+
+
+class plora_muon_state(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("eps", ctypes.c_float), ("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float),
+                ("ns_steps", ctypes.c_int32), ("nesterov", ctypes.c_int32), ("scale", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("A_master", ctypes.c_void_p), ("B_master", ctypes.c_void_p),
+                ("mA", ctypes.c_void_p), ("mB", ctypes.c_void_p)]
 
 
 class PloraError(RuntimeError):
@@ -129,6 +152,14 @@ def load(path: str = LIB_PATH):
     lib.plora_debug_timeout_probe.restype = ctypes.c_int
     lib.plora_adamw_step.argtypes = [H, I32, P, P, P]
     lib.plora_adamw_step.restype = ctypes.c_int
+    lib.plora_epilogue_work_bytes.argtypes = [H, I32, P, P, ctypes.POINTER(ctypes.c_size_t)]
+    lib.plora_forward_epilogue.argtypes = [H, P, P, P, I32, P, P, P, P, P]
+    lib.plora_backward_epilogue.argtypes = [H, P, P, P, P, I32, P, P, P, P, P]
+    lib.plora_muon_work_bytes.argtypes = [H, I32, P, ctypes.POINTER(ctypes.c_size_t)]
+    lib.plora_muon_step.argtypes = [H, I32, P, P, P, P]
+    for fn in ("plora_epilogue_work_bytes", "plora_forward_epilogue", "plora_backward_epilogue",
+               "plora_muon_work_bytes", "plora_muon_step"):
+        getattr(lib, fn).restype = ctypes.c_int
     lib.plora_grad_B_static.argtypes = [ctypes.POINTER(plora_config), P, I32, P, P, P, P]
     lib.plora_grad_B_static.restype = ctypes.c_int
     lib.plora_version.argtypes = []
@@ -366,6 +397,84 @@ def plora_adamw_step(h: int, n: int, tab, states, stream: int = 0, check: bool =
     return s
 
 
+def make_muon_states(hparams, A_master, B_master, mA, mB):
+    """Host plora_muon_state[] from per-adapter dicts (lr; momentum 0.95, nesterov True, weight_decay 0,
+    eps 1e-7, ns_steps 5, coeffs MUON_COEFFS, scale "rows": "none", "rows" or "rms") and device pointers
+    (ints; A_master / B_master None for an fp32 handle)."""
+    st = (plora_muon_state * max(1, len(hparams)))()
+    for i, hp in enumerate(hparams):
+        st[i].lr = float(hp["lr"])
+        st[i].momentum = float(hp.get("momentum", 0.95))
+        st[i].weight_decay = float(hp.get("weight_decay", 0.0))
+        st[i].eps = float(hp.get("eps", 1e-7))
+        st[i].a, st[i].b, st[i].c = (float(x) for x in hp.get("coeffs", MUON_COEFFS))
+        st[i].ns_steps = int(hp.get("ns_steps", 5))
+        st[i].nesterov = int(bool(hp.get("nesterov", True)))
+        st[i].scale = MUON_SCALES[hp.get("scale", "rows")]
+        st[i].A_master = A_master[i] if A_master is not None else None
+        st[i].B_master = B_master[i] if B_master is not None else None
+        st[i].mA, st[i].mB = mA[i], mB[i]
+    return st
+
+
+def plora_muon_work_bytes(h: int, n: int, tab) -> int:
+    out = ctypes.c_size_t(0)
+    _raise(h, load().plora_muon_work_bytes(h, n, ctypes.addressof(tab), ctypes.byref(out)))
+    return int(out.value)
+
+
+def plora_muon_step(h: int, n: int, tab, states, work: int, stream: int = 0, check: bool = True) -> int:
+    s = load().plora_muon_step(h, n, ctypes.addressof(tab), ctypes.addressof(states), work or None, stream)
+    if check:
+        _raise(h, s)
+    return s
+
+
+def make_epilogue(activation="none", bias=None, dbias=None, residual=None, Z=None, work=None) -> plora_epilogue:
+    """plora_epilogue from an activation's name (or number) and device pointers (ints); bias and dbias are
+    lists with one pointer (or None) per adapter, or None."""
+    ep = plora_epilogue()
+    if isinstance(activation, str) and activation not in ACTIVATIONS:
+        raise ValueError(f"activation {activation!r}: one of {', '.join(ACTIVATIONS)}")
+    ep.activation = ACTIVATIONS[activation] if isinstance(activation, str) else int(activation)
+    keep = []
+    for name, ptrs in (("bias", bias), ("dbias", dbias)):
+        if ptrs is not None:
+            arr = (ctypes.c_void_p * max(1, len(ptrs)))(*ptrs)
+            keep.append(arr)
+            setattr(ep, name, ctypes.addressof(arr))
+    ep.residual, ep.Z, ep.work = residual or None, Z or None, work or None
+    ep._keep = keep
+    return ep
+
+
+def plora_epilogue_work_bytes(h: int, n: int, off, ep: plora_epilogue) -> int:
+    off = _offsets(off)
+    out = ctypes.c_size_t(0)
+    _raise(h, load().plora_epilogue_work_bytes(h, n, off.ctypes.data, ctypes.addressof(ep), ctypes.byref(out)))
+    return int(out.value)
+
+
+def plora_forward_epilogue(h: int, X: int, W: int, Y: int, n: int, off, tab, saved: int, ep: plora_epilogue,
+                           stream: int = 0, check: bool = True) -> int:
+    off = _offsets(off)
+    s = load().plora_forward_epilogue(h, X, W, Y, n, off.ctypes.data, ctypes.addressof(tab), saved,
+                                      ctypes.addressof(ep), stream)
+    if check:
+        _raise(h, s)
+    return s
+
+
+def plora_backward_epilogue(h: int, X: int, W: int, dY: int, dX: Optional[int], n: int, off, tab, saved: int,
+                            ep: plora_epilogue, stream: int = 0, check: bool = True) -> int:
+    off = _offsets(off)
+    s = load().plora_backward_epilogue(h, X, W, dY, dX or None, n, off.ctypes.data, ctypes.addressof(tab), saved,
+                                       ctypes.addressof(ep), stream)
+    if check:
+        _raise(h, s)
+    return s
+
+
 def plora_debug_timeout_probe(h: int, timeout_ns: int, stream: int = 0) -> int:
     return int(load().plora_debug_timeout_probe(h, int(timeout_ns), stream))
 
@@ -443,6 +552,96 @@ class PackedLoRA:
         plora_backward(self.h, X.data_ptr(), W.data_ptr(), dY.data_ptr(), dX.data_ptr() if want_dX else None,
                        n, off, tab, saved.data_ptr(), st)
         return dX, dA, dB
+
+    def _check_tensors(self, T, **named):
+        """Shapes, dtype and layout of the tensors an epilogue call takes by pointer."""
+        import torch
+        dt = torch.bfloat16 if self.dtype == "bf16" else torch.float32
+        shape = {"X": (T, self.d_in), "W": (self.d_out, self.d_in), "bias": (self.d_out,)}
+        for name, t in named.items():
+            if t is None:
+                continue
+            want = shape.get(name, (T, self.d_out))
+            if tuple(t.shape) != want or t.dtype != dt or not t.is_contiguous():
+                raise ValueError(f"{name}: a contiguous {dt} tensor of shape {want} is needed, got {t.dtype} "
+                                 f"{tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous'}")
+
+    def _check_factors(self, A, B, n):
+        import torch
+        dt = torch.bfloat16 if self.dtype == "bf16" else torch.float32
+        P = len(self.out_blocks) if self.out_blocks else 1
+        if len(A) != n or len(B) != n:
+            raise ValueError(f"{len(A)} A and {len(B)} B factors for {n} adapters")
+        for i, (a, b) in enumerate(zip(A, B)):
+            r = b.shape[1]
+            if tuple(a.shape) != (P * r, self.d_in) or tuple(b.shape) != (self.d_out, r) or a.dtype != dt \
+                    or b.dtype != dt or not a.is_contiguous() or not b.is_contiguous():
+                raise ValueError(f"adapter {i}: contiguous {dt} factors A {(P * r, self.d_in)} and B "
+                                 f"{(self.d_out, r)} are needed, got {tuple(a.shape)} and {tuple(b.shape)}")
+
+    def _bias_list(self, bias, n):
+        """One bias (or None) per adapter from None, one tensor for every adapter, or a list."""
+        if bias is None:
+            return None
+        out = list(bias) if isinstance(bias, (list, tuple)) else [bias] * n
+        if len(out) != n:
+            raise ValueError(f"bias: {len(out)} entries for {n} adapters")
+        for b in out:
+            self._check_tensors(0, bias=b)
+        return out
+
+    def forward_epilogue(self, X, W, off, scales, A, B, bias=None, activation="none", residual=None, want_Z=True,
+                         Y=None, saved=None, stream=None):
+        """Y = act(X W + s (X A) B + bias) + residual; returns (Y, saved, Z).
+
+        bias: one ``[d_out]`` tensor for every adapter, a list with one (or None) per adapter, or None;
+        activation: a name in ``ACTIVATIONS``; residual: ``[T][d_out]`` (with a bf16 engine it may be the tensor
+        given as Y).
+        Z, the pre-activation that ``backward_epilogue`` needs, is kept if there is an activation and
+        want_Z is true, else None."""
+        import torch
+        n = len(off) - 1
+        self._check_tensors(X.shape[0], X=X, W=W, residual=residual, Y=Y)
+        bias = self._bias_list(bias, n)
+        self._check_factors(A, B, n)
+        tab = self.table(scales, A, B)
+        if Y is None:
+            Y = torch.empty((X.shape[0], self.d_out), dtype=X.dtype, device=X.device)
+        if saved is None:
+            saved = torch.empty(max(self.saved_bytes(off, tab), 256), dtype=torch.uint8, device=X.device)
+        Z = torch.empty_like(Y) if want_Z and activation != "none" else None
+        ep = make_epilogue(activation, None if bias is None else [b.data_ptr() if b is not None else None for b in bias],
+                           residual=residual.data_ptr() if residual is not None else None,
+                           Z=Z.data_ptr() if Z is not None else None)
+        st = (stream or torch.cuda.current_stream(X.device)).cuda_stream
+        plora_forward_epilogue(self.h, X.data_ptr(), W.data_ptr(), Y.data_ptr(), n, off, tab, saved.data_ptr(), ep, st)
+        return Y, saved, Z
+
+    def backward_epilogue(self, X, W, dY, off, scales, A, B, saved, Z=None, activation="none", want_dX=True,
+                          want_dbias=False, stream=None):
+        """The backward of ``forward_epilogue``: returns (dX, dA, dB, dbias).  dX is None without want_dX;
+        dbias is a list of fp32 ``[d_out]`` tensors, one per adapter, or None; want_dbias may be a list of
+        truth values, one per adapter (dbias[i] is then None where it is false).  The residual's gradient
+        is dY."""
+        import torch
+        n = len(off) - 1
+        self._check_tensors(X.shape[0], X=X, W=W, dY=dY, Z=Z)
+        self._check_factors(A, B, n)
+        f32 = dict(dtype=torch.float32, device=X.device)
+        dA, dB = [torch.empty(a.shape, **f32) for a in A], [torch.empty(b.shape, **f32) for b in B]
+        dX = torch.empty_like(X) if want_dX else None
+        want = list(want_dbias) if isinstance(want_dbias, (list, tuple)) else [bool(want_dbias)] * n
+        db = [torch.empty(self.d_out, **f32) if w else None for w in want] if any(want) else None
+        tab = self.table(scales, A, B, dA, dB)
+        ep = make_epilogue(activation, dbias=None if db is None else [b.data_ptr() if b is not None else None for b in db],
+                           Z=Z.data_ptr() if Z is not None else None)
+        nbytes = plora_epilogue_work_bytes(self.h, n, off, ep)
+        work = torch.empty(nbytes, dtype=torch.uint8, device=X.device) if nbytes else None
+        ep.work = work.data_ptr() if work is not None else None
+        st = (stream or torch.cuda.current_stream(X.device)).cuda_stream
+        plora_backward_epilogue(self.h, X.data_ptr(), W.data_ptr(), dY.data_ptr(), dX.data_ptr() if want_dX else None,
+                                n, off, tab, saved.data_ptr(), ep, st)
+        return dX, dA, dB, db
 
 
 # ---------------------------------------------------------------- layer calls
@@ -566,34 +765,57 @@ class PackedLoRALayer:
 
 
 # ---------------------------------------------------------------- autograd
-def packed_lora(engine: "PackedLoRA", X, W, off, scales, A, B):
-    """Y = X W + s_i (X_i A_i) B_i for every packed adapter, differentiable in X, A_i and B_i
-    (W is the frozen base weight and gets no gradient).  A[i] is lora_A.weight ([r_i][d_in]),
-    B[i] is lora_B.weight ([d_out][r_i]), W is nn.Linear.weight ([d_out][d_in]); `off` holds
-    the host segment offsets of the packed rows of X.  The backward runs plora_backward; the
-    fp32 weight gradients are returned in each parameter's dtype."""
+def packed_lora(engine: "PackedLoRA", X, W, off, scales, A, B, bias=None, activation="none", residual=None):
+    """Y = act(X W + s_i (X_i A_i) B_i + b_i) + residual for every packed adapter, differentiable in X,
+    A_i, B_i, b_i and residual (W is the frozen base weight and gets no gradient).  A[i] is lora_A.weight
+    ([r_i][d_in]), B[i] is lora_B.weight ([d_out][r_i]), W is nn.Linear.weight ([d_out][d_in]); `off` holds
+    the host segment offsets of the packed rows of X.  bias: None, one [d_out] tensor that every adapter
+    shares (its gradient sums over the adapters) or a list with one (or None) per adapter; activation: a
+    name in ACTIVATIONS; residual: [T][d_out].  Without these three the backward runs plora_backward, else
+    plora_backward_epilogue; the fp32 weight gradients are returned in each parameter's dtype."""
     import torch
+    n = len(off) - 1
+    plain = bias is None and activation == "none" and residual is None
+    per_adapter = [None] * n if bias is None else engine._bias_list(bias, n)
+    uniq = list({id(b): b for b in per_adapter if b is not None}.values())   # a shared bias is one input
+    where = [next((k for k, u in enumerate(uniq) if u is b), None) for b in per_adapter]
 
     class _PackedLoRAFn(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, X_, W_, *AB):
-            n = len(off) - 1
-            A_, B_ = list(AB[:n]), list(AB[n:])
-            Y, saved = engine.forward(X_.contiguous(), W_.contiguous(), off, scales, A_, B_)
-            ctx.save_for_backward(X_, W_, saved, *AB)
+        def forward(ctx, X_, W_, R_, *ABb):
+            A_, B_, b_ = list(ABb[:n]), list(ABb[n:2 * n]), ABb[2 * n:]
+            X_, W_, Z = X_.contiguous(), W_.contiguous(), None
+            if plain:
+                Y, saved = engine.forward(X_, W_, off, scales, A_, B_)
+            else:
+                Y, saved, Z = engine.forward_epilogue(X_, W_, off, scales, A_, B_,
+                                                      bias=[None if k is None else b_[k] for k in where],
+                                                      activation=activation,
+                                                      residual=None if R_ is None else R_.contiguous())
+            ctx.save_for_backward(X_, W_, saved, Z, *ABb[:2 * n])
             return Y
 
         @staticmethod
         def backward(ctx, dY):
-            X_, W_, saved, *AB = ctx.saved_tensors
-            n = len(off) - 1
+            X_, W_, saved, Z, *AB = ctx.saved_tensors
             A_, B_ = list(AB[:n]), list(AB[n:])
-            dX, dA, dB = engine.backward(X_, W_, dY.contiguous(), off, scales, A_, B_, saved,
-                                         want_dX=ctx.needs_input_grad[0])
+            need_b = ctx.needs_input_grad[3 + 2 * n:]
+            gb = [None] * len(uniq)
+            if plain:
+                dX, dA, dB = engine.backward(X_, W_, dY.contiguous(), off, scales, A_, B_, saved,
+                                             want_dX=ctx.needs_input_grad[0])
+            else:
+                dX, dA, dB, db = engine.backward_epilogue(X_, W_, dY.contiguous(), off, scales, A_, B_, saved, Z=Z,
+                                                          activation=activation, want_dX=ctx.needs_input_grad[0],
+                                                          want_dbias=[k is not None and need_b[k] for k in where])
+                for k, u in enumerate(uniq):   # a shared bias sums its adapters' fp32 gradients
+                    if need_b[k]:
+                        own = [db[i] for i in range(n) if where[i] == k]
+                        gb[k] = (own[0] if len(own) == 1 else torch.stack(own).sum(0)).to(u.dtype)
             gA = [g.to(a.dtype) for g, a in zip(dA, A_)]
             gB = [g.to(b.dtype) for g, b in zip(dB, B_)]
-            return (dX, None, *gA, *gB)
+            return (dX, None, dY if ctx.needs_input_grad[2] else None, *gA, *gB, *gb)
 
     if W.requires_grad:
         raise ValueError("packed_lora: the base weight W is frozen; pass W with requires_grad=False")
-    return _PackedLoRAFn.apply(X, W, *A, *B)
+    return _PackedLoRAFn.apply(X, W, residual, *A, *B, *uniq)

@@ -24,6 +24,8 @@
 #include "tc.cuh"
 #include "tc_pair.cuh"
 #include "adamw.cuh"
+#include "epilogue.cuh"
+#include "muon.cuh"
 
 using namespace plora;
 
@@ -99,8 +101,8 @@ struct plora_ctx {
 
     // Launch accounting and optional per-kernel timing (CUDA events on the launching stream).
     bool profiling = false;
-    int64_t launches[16] = {};
-    double total_ms[16] = {};
+    int64_t launches[32] = {};
+    double total_ms[32] = {};
     struct Rec { int kind; cudaEvent_t a, b; };
     std::vector<Rec> pending;
     std::vector<cudaEvent_t> pool;
@@ -146,6 +148,20 @@ bool get_encode() {
     return true;
 }
 
+// Makes a handle's device current for one call and puts the caller's back at its end.
+struct DeviceGuard {
+    int prev = -1;
+    cudaError_t enter(int device) {
+        cudaError_t e = cudaGetDevice(&prev);
+        if (e != cudaSuccess) { prev = -1; return e; }
+        if (prev == device) { prev = -1; return cudaSuccess; }
+        return cudaSetDevice(device);
+    }
+    ~DeviceGuard() {
+        if (prev >= 0) cudaSetDevice(prev);
+    }
+};
+
 // [p, p + bytes) must lie inside one device allocation: every tensor pointer is checked against the
 // driver's record of the allocation that contains it, so that no kernel is ever launched on a host
 // pointer, an unallocated address or a buffer that is too small.
@@ -160,6 +176,26 @@ bool get_range_fn() {
         return false;
     g_range = reinterpret_cast<PFN_cuMemGetAddressRange_v3020>(fn);
     return true;
+}
+
+// A buffer of a call, for the check that nothing the call writes overlaps anything else it touches.
+struct Span {
+    uintptr_t at;
+    size_t bytes;
+    bool write;
+};
+
+// Two spans overlap and at least one of them is written.
+bool spans_clash(std::vector<Span>& v) {
+    std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.at < b.at; });
+    uintptr_t end_any = 0, end_write = 0;   // the furthest ends of the spans so far, and of the written ones
+    for (const Span& s : v) {
+        if (s.bytes == 0) continue;
+        if (s.at < (s.write ? end_any : end_write)) return true;
+        end_any = std::max(end_any, s.at + s.bytes);
+        if (s.write) end_write = std::max(end_write, s.at + s.bytes);
+    }
+    return false;
 }
 
 bool in_device_allocation(const void* p, size_t bytes) {
@@ -189,10 +225,13 @@ __global__ void timeout_probe_kernel(int* err_flag, uint64_t limit_ns) {
 
 // Kernel kinds for launch accounting / profiling.
 enum Kind { kPack = 0, kBaseFwd, kShrinkX, kExpandY, kBaseDx, kShrinkDy, kExpandDx, kWgradB, kWgradA,
-            kSimt, kAdamw, kShrinkDyWgradB, kStage, kBaseDxWgradA, kKinds };
+            kSimt, kAdamw, kShrinkDyWgradB, kStage, kBaseDxWgradA, kBaseFwdEp, kEpilogue, kActGrad, kBiasGrad,
+            kMuonGramK, kMuonNsK, kMuonApplyK, kKinds };
 const char* const kKindNames[kKinds] = {"pack_ab", "base_fwd", "shrink_x", "expand_y", "base_dx",
                                         "shrink_dy", "expand_dx", "wgrad_b", "wgrad_a", "simt_gemm", "adamw",
-                                        "shrink_dy+wgrad_b", "stage_copy", "base_dx+wgrad_a"};
+                                        "shrink_dy+wgrad_b", "stage_copy", "base_dx+wgrad_a", "base_fwd_ep",
+                                        "epilogue", "act_grad", "bias_grad", "muon_gram", "muon_ns", "muon_apply"};
+static_assert(kKinds <= 32, "plora_ctx::launches and total_ms hold every kind");
 
 cudaEvent_t take_event(plora_ctx* h) {
     if (!h->pool.empty()) {
@@ -249,11 +288,10 @@ struct HostPlan {
     int32_t slots = 0, counters = 0;
 };
 
-plora_status check_table(plora_ctx* h, int32_t n, const int64_t* off, const plora_adapter* tab, bool grads) {
+plora_status check_offsets(plora_ctx* h, int32_t n, const int64_t* off) {
     if (n < 0 || n > h->cfg.max_adapters)
         return fail(h, PLORA_ERR_INVALID_ARG, "n_adapters=%d outside [0, max_adapters=%d]", n, h->cfg.max_adapters);
     if (!off) return fail(h, PLORA_ERR_INVALID_ARG, "off is NULL");
-    if (n > 0 && !tab) return fail(h, PLORA_ERR_INVALID_ARG, "adapter table is NULL");
     if (off[0] != 0) return fail(h, PLORA_ERR_INVALID_ARG, "off[0]=%lld, must be 0", (long long)off[0]);
     for (int32_t i = 0; i < n; ++i) {
         if (off[i + 1] < off[i])
@@ -263,6 +301,13 @@ plora_status check_table(plora_ctx* h, int32_t n, const int64_t* off, const plor
     if (off[n] > h->cfg.max_tokens)
         return fail(h, PLORA_ERR_INVALID_ARG, "off[n]=%lld exceeds max_tokens=%lld", (long long)off[n],
                     (long long)h->cfg.max_tokens);
+    return PLORA_OK;
+}
+
+plora_status check_table(plora_ctx* h, int32_t n, const int64_t* off, const plora_adapter* tab, bool grads) {
+    const plora_status s = check_offsets(h, n, off);
+    if (s != PLORA_OK) return s;
+    if (n > 0 && !tab) return fail(h, PLORA_ERR_INVALID_ARG, "adapter table is NULL");
     for (int32_t i = 0; i < n; ++i) {
         const plora_adapter& a = tab[i];
         if (a.rank < 1 || a.rank > h->cfg.max_rank)
@@ -431,7 +476,22 @@ struct DevPlan {
     MTileRec* mt_rec = nullptr;
     LoraSeg* mt_seg = nullptr;
     int32_t* dyn = nullptr;   // kDynCounters item counters, zero when the call's launches start
+    const void* const* bias = nullptr;   // the epilogue's per-adapter tables (null: none)
+    float* const* dbias = nullptr;
+    const int32_t* tile0 = nullptr;
     int slot = 0;
+};
+
+// A call's epilogue as the host checked it (plora_epilogue), with the tables the kernels read.
+struct EpiTables {
+    bool on = false;
+    int32_t act = 0;
+    const void* residual = nullptr;
+    void* Z = nullptr;
+    void* work = nullptr;
+    std::vector<const void*> bias;   // per adapter, empty when no adapter has one
+    std::vector<float*> dbias;       // per adapter, empty when none is wanted
+    std::vector<int32_t> tile0;      // per adapter: its first 128-row tile
 };
 
 // Copies calls' schedules from their slots' mapped pinned staging buffers into device memory, one
@@ -526,7 +586,7 @@ plora_status take_slot(plora_ctx* h, cudaStream_t st, Slot& sl) {
 // With `defer`, the copy is queued there instead of launched (a layer call stages every projection's
 // schedule with one launch).
 plora_status upload(plora_ctx* h, const HostPlan& P, const std::vector<SimtOp>& ops, cudaStream_t st,
-                    DevPlan& D, StageCopies* defer = nullptr) {
+                    DevPlan& D, StageCopies* defer = nullptr, const EpiTables* ep = nullptr) {
     Slot sl;
     plora_status ps = take_slot(h, st, sl);
     if (ps != PLORA_OK) return ps;
@@ -545,6 +605,9 @@ plora_status upload(plora_ctx* h, const HostPlan& P, const std::vector<SimtOp>& 
     const size_t o_mtl = put(P.mt_seg.data(), P.mt_seg.size() * sizeof(LoraSeg));
     const int32_t zeros[kDynCounters] = {};
     const size_t o_dyn = put(zeros, sizeof(zeros));   // the schedule copy clears the item counters
+    const size_t o_bias = ep ? put(ep->bias.data(), ep->bias.size() * sizeof(void*)) : 0;
+    const size_t o_db = ep ? put(ep->dbias.data(), ep->dbias.size() * sizeof(float*)) : 0;
+    const size_t o_t0 = ep ? put(ep->tile0.data(), ep->tile0.size() * sizeof(int32_t)) : 0;
     if (o > h->blob_bytes) return fail(h, PLORA_ERR_INVALID_ARG, "schedule exceeds the handle's staging size");
     uint8_t* d = sl.dev;
     if (defer) {
@@ -560,6 +623,11 @@ plora_status upload(plora_ctx* h, const HostPlan& P, const std::vector<SimtOp>& 
     D.mt_rec = reinterpret_cast<MTileRec*>(d + o_mto);
     D.mt_seg = reinterpret_cast<LoraSeg*>(d + o_mtl);
     D.dyn = reinterpret_cast<int32_t*>(d + o_dyn);
+    if (ep) {
+        if (!ep->bias.empty()) D.bias = reinterpret_cast<const void* const*>(d + o_bias);
+        if (!ep->dbias.empty()) D.dbias = reinterpret_cast<float* const*>(d + o_db);
+        D.tile0 = reinterpret_cast<const int32_t*>(d + o_t0);
+    }
     D.slot = sl.index;
     return PLORA_OK;
 }
@@ -651,11 +719,11 @@ int seg_finish(Segments& S) {
     return S.g.begin[S.g.n_seg];
 }
 
-template <Op OP, Op OP2 = OP>
+template <Op OP, Op OP2 = OP, bool EP = false>
 cudaError_t launch_segments(Segments& S, int num_sms, cudaStream_t st) {
     const int total = seg_finish(S);
     if (total <= 0) return cudaSuccess;
-    tc_kernel<OP, OP2><<<std::min(total, num_sms), kTcThreads, kTcSmemBytes, st>>>(S.m, S.g);
+    tc_kernel<OP, OP2, EP><<<std::min(total, num_sms), kTcThreads, kTcSmemBytes, st>>>(S.m, S.g);
     return cudaGetLastError();
 }
 
@@ -761,9 +829,9 @@ void base_tiles(TcParams& p, int64_t T, int64_t N, int window_rows) {
     }
 }
 
-template <Op OP, Op OP2 = OP>
+template <Op OP, Op OP2 = OP, bool EP = false>
 cudaError_t set_tc_attr() {
-    return cudaFuncSetAttribute(tc_kernel<OP, OP2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmemBytes);
+    return cudaFuncSetAttribute(tc_kernel<OP, OP2, EP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmemBytes);
 }
 
 TcParams base_params(const plora_ctx* h, const HostPlan& P, const DevPlan& D) {
@@ -907,9 +975,10 @@ struct FwdCall {
     const void* W = nullptr;
     void* Y = nullptr;
     void* saved = nullptr;
+    EpiTables ep;              // the projection's epilogue (off for a plain forward)
     HostPlan P;
     DevPlan D;
-    CUtensorMap mX, mXb, mW, mW128, mPA16, mPA32, mPA64, mPA128, mHk, mHkb, mPBk, mPBk128, mY;
+    CUtensorMap mZ, mX, mXb, mW, mW128, mPA16, mPA32, mPA64, mPA128, mHk, mHkb, mPBk, mPBk128, mY;
     TcParams q{}, p{};
 };
 
@@ -918,7 +987,7 @@ struct FwdCall {
 plora_status fwd_prepare(FwdCall& c, cudaStream_t st, StageCopies& cs) {
     plora_ctx* h = c.h;
     const HostPlan& P = c.P;
-    plora_status s = upload(h, P, {}, st, c.D, &cs);
+    plora_status s = upload(h, P, {}, st, c.D, &cs, c.ep.on ? &c.ep : nullptr);
     if (s != PLORA_OK) return s;
     const int64_t d_in = h->cfg.d_in, d_out = h->cfg.d_out;
     // mPA16 .. mPA128: the A pack in boxes of 16 to 128 rows (the shrink's K-major B, an adapter's rows
@@ -929,6 +998,7 @@ plora_status fwd_prepare(FwdCall& c, cudaStream_t st, StageCopies& cs) {
     const uint8_t* sv = static_cast<const uint8_t*>(c.saved);
     bool ok = make_map(&c.mX, c.X, d_in, P.T, d_in, 64, kTileM) &&
               make_map(&c.mY, c.Y, d_out, P.T, d_out, 64, 32) &&
+              (!c.ep.Z || make_map(&c.mZ, c.ep.Z, d_out, P.T, d_out, 64, 32)) &&
               make_map(&c.mW, c.W, d_in, d_out, d_in, 64, kTileN) &&
               make_map(&c.mW128, c.W, d_in, d_out, d_in, 64, kTileM) &&
               make_map(&c.mPA16, sv + L.o_packA, d_in, (uint64_t)P.n * P.RP, d_in, 64, 16) &&
@@ -1030,6 +1100,14 @@ plora_status fwd_launch(FwdCall* calls, int nc, cudaStream_t st, StageCopies& cs
             FwdCall& c = calls[k];
             S = Segments{};
             seg_add(S, c.p, SegMaps{&c.mXb, &c.mW, &c.mHkb, &c.mPBk, &c.mY}, false);
+            if (c.ep.on) {
+                S.g.ep = EpiFused{c.ep.act, c.ep.Z ? 1 : 0, c.D.bias, static_cast<const __nv_bfloat16*>(c.ep.residual)};
+                S.m.m[1][0] = c.ep.Z ? c.mZ : c.mY;
+                tracked(h0, kBaseFwdEp, st, [&] {
+                    launch_segments<Op::BaseFwd, Op::BaseFwd, true>(S, h0->num_sms, st);
+                });
+                continue;
+            }
             tracked(h0, kBaseFwd, st, [&] { launch_segments<Op::BaseFwd>(S, h0->num_sms, st); });
         }
     }
@@ -1040,6 +1118,57 @@ plora_status fwd_launch(FwdCall* calls, int nc, cudaStream_t st, StageCopies& cs
     return PLORA_OK;
 }
 
+// Bytes of the backward's scratch: dZ [T][d_out] (with an activation), then the tile sums of the bias
+// gradient, [tiles][d_out] fp32.
+struct EpiWork {
+    size_t o_part = 0, bytes = 0;
+};
+EpiWork epi_work(const plora_ctx* h, int64_t T, int64_t tiles, bool act, bool dbias) {
+    EpiWork w;
+    const size_t d_out = (size_t)h->cfg.d_out;
+    w.o_part = act ? (size_t)round_up((int64_t)((size_t)T * d_out * h->esize), 256) : 0;
+    w.bytes = w.o_part + (dbias ? (size_t)tiles * d_out * sizeof(float) : 0);
+    return w;
+}
+
+// dZ = dY act'(Z) into the work buffer and every wanted db_i (nothing to do without either).
+template <typename T>
+void epilogue_grad(plora_ctx* h, const HostPlan& P, const DevPlan& D, const EpiTables& ep, const void* dY,
+                   cudaStream_t st) {
+    const bool act = ep.act != kActNone, db = D.dbias != nullptr;
+    if (!act && !db) return;
+    const EpiWork w = epi_work(h, P.T, (int64_t)P.tok.size(), act, db);
+    const unsigned cols = (unsigned)ceil_div(h->cfg.d_out, kEpiCols);
+    float* part = db ? reinterpret_cast<float*>(static_cast<uint8_t*>(ep.work) + w.o_part) : nullptr;
+    ActGradArgs a{ep.act, 0, h->cfg.d_out, D.tok, dY, act ? ep.Z : nullptr, act ? ep.work : nullptr, part};
+    // grid.y holds at most 65535 tiles: longer buffers take several launches
+    const int64_t tiles = (int64_t)P.tok.size();
+    for (int64_t t0 = 0; t0 < tiles; t0 += 65535) {
+        a.tok = D.tok + t0;
+        a.part = part ? part + t0 * h->cfg.d_out : nullptr;
+        const unsigned ny = (unsigned)std::min<int64_t>(65535, tiles - t0);
+        tracked(h, kActGrad, st, [&] { act_grad_kernel<T><<<dim3(cols, ny), 256, 0, st>>>(a); });
+    }
+    if (db)
+        tracked(h, kBiasGrad, st, [&] {
+            bias_grad_kernel<<<dim3(cols, (unsigned)P.n), 256, 0, st>>>(D.ad, D.dbias, D.tile0, part, h->cfg.d_out);
+        });
+}
+
+// The fp32 path's epilogue, in place on Y.
+template <typename T>
+void epilogue_apply(plora_ctx* h, const HostPlan& P, const DevPlan& D, const EpiTables& ep, void* Y, cudaStream_t st) {
+    EpiArgs a{ep.act, P.n, h->cfg.d_out, D.tok, D.bias, ep.residual, Y, ep.Z};
+    const int64_t tiles = (int64_t)P.tok.size();
+    for (int64_t t0 = 0; t0 < tiles; t0 += 65535) {
+        a.tok = D.tok + t0;
+        const unsigned ny = (unsigned)std::min<int64_t>(65535, tiles - t0);
+        tracked(h, kEpilogue, st, [&] {
+            epilogue_kernel<T><<<dim3((unsigned)ceil_div(h->cfg.d_out, kEpiCols), ny), 256, 0, st>>>(a);
+        });
+    }
+}
+
 struct BwdCall {
     plora_ctx* h = nullptr;
     const void* X = nullptr;
@@ -1047,6 +1176,8 @@ struct BwdCall {
     const void* dY = nullptr;
     void* dX = nullptr;
     const void* saved = nullptr;
+    const void* dY_in = nullptr;   // with an epilogue: the caller's dY (dY above is then the work buffer's dZ)
+    EpiTables ep;
     HostPlan P;
     DevPlan D;
     CUtensorMap mdY_k, mdY_kb, mdY_mn, mW_mn, mPB_mn, mG_k, mG_kb, mG_mn, mPA_mn, mPA16, mH_mn, mX_mn, mdX;
@@ -1059,7 +1190,7 @@ struct BwdCall {
 plora_status bwd_prepare(BwdCall& c, cudaStream_t st, StageCopies& cs) {
     plora_ctx* h = c.h;
     const HostPlan& P = c.P;
-    plora_status s = upload(h, P, {}, st, c.D, &cs);
+    plora_status s = upload(h, P, {}, st, c.D, &cs, c.ep.on ? &c.ep : nullptr);
     if (s != PLORA_OK) return s;
     const int64_t d_in = h->cfg.d_in, d_out = h->cfg.d_out;
     void* G = h->at<void>(h->r_G);
@@ -1126,6 +1257,8 @@ plora_status bwd_launch(BwdCall* calls, int nc, cudaStream_t st, StageCopies& cs
     if (e != cudaSuccess) return cuda_fail(h0, e, "copying the schedule to the device");
     int RPmax = kRankAlign;
     for (int k = 0; k < nc; ++k) RPmax = std::max(RPmax, calls[k].P.RP);
+    for (int k = 0; k < nc; ++k)
+        if (calls[k].ep.on) epilogue_grad<__nv_bfloat16>(calls[k].h, calls[k].P, calls[k].D, calls[k].ep, calls[k].dY_in, st);
     Segments& S = *h0->segs;
     S = Segments{};
     // G's shrink reduces over d_out, the dX GEMM too: the calls with the widest d_out first
@@ -1193,6 +1326,388 @@ plora_status bwd_launch(BwdCall* calls, int nc, cudaStream_t st, StageCopies& cs
         if (s != PLORA_OK) return s;
     }
     return PLORA_OK;
+}
+
+// The checks of a forward's (dY: the call's Y) or a backward's epilogue; fills the tables its kernels read.
+plora_status epilogue_args(plora_ctx* h, const HostPlan& P, const plora_epilogue& e, bool backward, const void* Y,
+                           const void* dX, EpiTables& ep) {
+    if (!h->tc && h->cfg.dtype != PLORA_FP32)
+        return fail(h, PLORA_ERR_UNSUPPORTED, "an epilogue needs an fp32 handle or the tensor-core path");
+    if (h->cfg.flags & (PLORA_FLAG_UNFUSED | PLORA_FLAG_BASE_PAIR))
+        return fail(h, PLORA_ERR_UNSUPPORTED, "an epilogue needs the fused single-SM base GEMM");
+    if (e.activation < PLORA_ACT_NONE || e.activation > PLORA_ACT_SILU || e.reserved != 0)
+        return fail(h, PLORA_ERR_INVALID_ARG, "activation=%d, reserved=%d", e.activation, e.reserved);
+    const bool act = e.activation != PLORA_ACT_NONE;
+    const size_t es = h->esize, d_out = (size_t)h->cfg.d_out, ybytes = (size_t)P.T * d_out * es;
+    ep.on = true;
+    ep.act = e.activation;
+    std::vector<Span> spans;
+    auto buffer = [&](const void* p, size_t bytes, size_t align, bool write, const char* name) {
+        if ((reinterpret_cast<uintptr_t>(p) & (align - 1)) != 0)
+            return fail(h, PLORA_ERR_INVALID_ARG, "%s not %zu-byte aligned", name, align);
+        if (!in_device_allocation(p, bytes))
+            return fail(h, PLORA_ERR_INVALID_ARG, "%s is not a device buffer of %zu bytes", name, bytes);
+        spans.push_back(Span{reinterpret_cast<uintptr_t>(p), bytes, write});
+        return PLORA_OK;
+    };
+    plora_status s = PLORA_OK;
+    if (!get_range_fn()) return fail(h, PLORA_ERR_CUDA, "cuMemGetAddressRange is not available");
+    for (int32_t i = 0; i < P.n && s == PLORA_OK; ++i) {
+        const void* b = !backward && e.bias ? e.bias[i] : nullptr;
+        float* db = backward && e.dbias ? e.dbias[i] : nullptr;
+        if (b) {
+            s = buffer(b, d_out * es, 16, false, "a bias");
+            if (ep.bias.empty()) ep.bias.assign(P.n, nullptr);
+            ep.bias[i] = b;
+        }
+        if (db && s == PLORA_OK) {
+            s = buffer(db, d_out * sizeof(float), 16, true, "a dbias");
+            if (ep.dbias.empty()) ep.dbias.assign(P.n, nullptr);
+            ep.dbias[i] = db;
+        }
+    }
+    if (s != PLORA_OK) return s;
+    if (P.T > 0) {
+        spans.push_back(Span{reinterpret_cast<uintptr_t>(Y), ybytes, !backward});
+        if (!backward) {
+            ep.residual = e.residual;
+            ep.Z = e.Z;
+            // the residual may be Y itself where the base GEMM's epilogue adds it (an element's residual is
+            // read before the element is written); the fp32 path builds Z in Y first
+            if (e.residual && e.residual == Y && !h->tc)
+                return fail(h, PLORA_ERR_INVALID_ARG, "an fp32 handle's residual cannot be Y");
+            if (e.residual && e.residual != Y) {
+                s = buffer(e.residual, ybytes, 16, false, "the residual");
+            }
+            if (s == PLORA_OK && e.Z) s = buffer(e.Z, ybytes, 16, true, "Z");
+        } else {
+            if (act && !e.Z) return fail(h, PLORA_ERR_INVALID_ARG, "the backward of an activation needs Z");
+            ep.Z = act ? e.Z : nullptr;
+            if (act) s = buffer(e.Z, ybytes, 16, false, "Z");
+            const size_t wb = epi_work(h, P.T, (int64_t)P.tok.size(), act, !ep.dbias.empty()).bytes;
+            if (s == PLORA_OK && wb) {
+                if (!e.work) return fail(h, PLORA_ERR_INVALID_ARG, "the backward needs a work buffer of %zu bytes", wb);
+                s = buffer(e.work, wb, 256, true, "work");
+                ep.work = e.work;
+            }
+            if (s == PLORA_OK && dX)
+                spans.push_back(Span{reinterpret_cast<uintptr_t>(dX), (size_t)P.T * (size_t)h->cfg.d_in * es, true});
+        }
+        if (s != PLORA_OK) return s;
+    }
+    if (spans_clash(spans))
+        return fail(h, PLORA_ERR_INVALID_ARG, "a buffer that the call writes overlaps another of its epilogue's buffers");
+    int32_t t0 = 0;
+    ep.tile0.resize(P.n);
+    for (int32_t i = 0; i < P.n; ++i) {
+        ep.tile0[i] = t0;
+        t0 += (int32_t)ceil_div(P.ad[i].n, kTileM);
+    }
+    return PLORA_OK;
+}
+
+// plora_forward, with an epilogue if epi is not null.
+plora_status forward_call(plora_ctx* h, const void* X, const void* W, void* Y, int32_t n, const int64_t* off,
+                          const plora_adapter* tab, void* saved, const plora_epilogue* epi, void* stream) {
+    if (!h) return PLORA_ERR_INVALID_ARG;
+    h->last_error.clear();
+    HostPlan P;
+    plora_status s = fwd_args(h, X, W, Y, n, off, tab, saved, P);
+    if (s != PLORA_OK) return s;
+    EpiTables ep;
+    if (epi) {
+        s = epilogue_args(h, P, *epi, false, Y, nullptr, ep);
+        if (s != PLORA_OK) return s;
+    }
+    if (P.T == 0) return PLORA_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int64_t d_in = h->cfg.d_in, d_out = h->cfg.d_out;
+
+    if (!h->tc) {
+        std::vector<SimtOp> ops;
+        int32_t t1 = 0, t2 = 0;
+        const bool f32 = h->cfg.dtype == PLORA_FP32;
+        const size_t es = h->esize;
+        // K1: Y = X W.  K2: H'_i = s_i X_i A_i.
+        add_op(ops, t1, X, d_in, 1, W, 1, d_in, Y, d_out, 1, P.T, d_out, d_in, 1.f, false, f32);
+        for (const AdapterDev& a : P.ad) {
+            if (a.n == 0) continue;
+            add_op(ops, t1, (const uint8_t*)X + (size_t)a.x_row * d_in * es, d_in, 1, a.A, 1, d_in,
+                   (uint8_t*)saved + (size_t)a.h_row * P.RP * es, P.RP, 1, a.n, a.rank, d_in, a.scale, false, f32);
+        }
+        const int n1 = (int)ops.size();
+        // K3: Y_i += H'_i B_i.
+        for (const AdapterDev& a : P.ad) {
+            if (a.n == 0) continue;
+            add_op(ops, t2, (const uint8_t*)saved + (size_t)a.h_row * P.RP * es, P.RP, 1, a.B, 1, a.rank,
+                   (uint8_t*)Y + (size_t)a.x_row * d_out * es, d_out, 1, a.n, d_out, a.rank, 1.f, true, f32);
+        }
+        DevPlan D;
+        s = upload(h, P, ops, st, D, nullptr, ep.on ? &ep : nullptr);
+        if (s != PLORA_OK) return s;
+        if (f32) {
+            launch_simt<float>(h, D.ops, n1, t1, st);
+            launch_simt<float>(h, D.ops + n1, (int)ops.size() - n1, t2, st);
+        } else {
+            launch_simt<__nv_bfloat16>(h, D.ops, n1, t1, st);
+            launch_simt<__nv_bfloat16>(h, D.ops + n1, (int)ops.size() - n1, t2, st);
+        }
+        if (ep.on) epilogue_apply<float>(h, P, D, ep, Y, st);   // an epilogue needs an fp32 handle here
+        return finish(h, D, st);
+    }
+
+    // Tensor-core path.
+    FwdCall c;
+    c.h = h; c.X = X; c.W = W; c.Y = Y; c.saved = saved;
+    c.P = std::move(P);
+    c.ep = std::move(ep);
+    StageCopies cs{};
+    s = fwd_prepare(c, st, cs);
+    if (s != PLORA_OK) return s;
+    return fwd_launch(&c, 1, st, cs);
+}
+
+// plora_backward, with an epilogue if epi is not null.
+plora_status backward_call(plora_ctx* h, const void* X, const void* W, const void* dY, void* dX, int32_t n,
+                           const int64_t* off, const plora_adapter* tab, const void* saved, const plora_epilogue* epi,
+                           void* stream) {
+    if (!h) return PLORA_ERR_INVALID_ARG;
+    h->last_error.clear();
+    HostPlan P;
+    plora_status s = bwd_args(h, X, W, dY, dX, n, off, tab, saved, P);
+    if (s != PLORA_OK) return s;
+    EpiTables ep;
+    if (epi) {
+        s = epilogue_args(h, P, *epi, true, dY, dX, ep);
+        if (s != PLORA_OK) return s;
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int64_t d_in = h->cfg.d_in, d_out = h->cfg.d_out;
+    s = zero_empty_grads(h, P, tab, st);
+    if (s != PLORA_OK) return s;
+    for (int32_t i : P.empty)
+        if (!ep.dbias.empty() && ep.dbias[i]) {
+            cudaError_t ce = cudaMemsetAsync(ep.dbias[i], 0, (size_t)d_out * sizeof(float), st);
+            if (ce != cudaSuccess) return cuda_fail(h, ce, "cudaMemsetAsync(dbias of an empty adapter)");
+        }
+    if (P.T == 0) return PLORA_OK;
+    const void* dY_in = dY;
+    if (ep.on && ep.act != kActNone) dY = ep.work;   // the products below take dZ
+    void* G = h->at<void>(h->r_G);
+
+    if (!h->tc) {
+        std::vector<SimtOp> ops;
+        int32_t t1 = 0, t2 = 0;
+        const bool f32 = h->cfg.dtype == PLORA_FP32;
+        const size_t es = h->esize;
+        // Phase 1 -- K4: dX = dY W^T; K5: G_i = s_i dY_i B_i^T; K7: dB_i = dY_i^T H'_i.
+        if (dX) add_op(ops, t1, dY, d_out, 1, W, d_in, 1, dX, d_in, 1, P.T, d_in, d_out, 1.f, false, f32);
+        for (const AdapterDev& a : P.ad) {
+            if (a.n == 0) continue;
+            add_op(ops, t1, (const uint8_t*)dY + (size_t)a.x_row * d_out * es, d_out, 1, a.B, a.rank, 1,
+                   (uint8_t*)G + (size_t)a.h_row * P.RP * es, P.RP, 1, a.n, a.rank, d_out, a.scale, false, f32);
+            add_op(ops, t1, (const uint8_t*)dY + (size_t)a.x_row * d_out * es, 1, d_out,
+                   (const uint8_t*)saved + (size_t)a.h_row * P.RP * es, P.RP, 1, a.dB, a.rank, 1, d_out, a.rank,
+                   a.n, 1.f, false, true);
+        }
+        const int n1 = (int)ops.size();
+        // Phase 2 -- K6: dX_i += G_i A_i^T; K8: dA_i = X_i^T G_i.
+        for (const AdapterDev& a : P.ad) {
+            if (a.n == 0) continue;
+            if (dX)
+                add_op(ops, t2, (const uint8_t*)G + (size_t)a.h_row * P.RP * es, P.RP, 1, a.A, d_in, 1,
+                       (uint8_t*)dX + (size_t)a.x_row * d_in * es, d_in, 1, a.n, d_in, a.rank, 1.f, true, f32);
+            add_op(ops, t2, (const uint8_t*)X + (size_t)a.x_row * d_in * es, 1, d_in,
+                   (const uint8_t*)G + (size_t)a.h_row * P.RP * es, P.RP, 1, a.dA, 1, d_in, d_in, a.rank, a.n,
+                   1.f, false, true);
+        }
+        DevPlan D;
+        s = upload(h, P, ops, st, D, nullptr, ep.on ? &ep : nullptr);
+        if (s != PLORA_OK) return s;
+        if (ep.on) epilogue_grad<float>(h, P, D, ep, dY_in, st);   // an epilogue needs an fp32 handle here
+        if (f32) {
+            launch_simt<float>(h, D.ops, n1, t1, st);
+            launch_simt<float>(h, D.ops + n1, (int)ops.size() - n1, t2, st);
+        } else {
+            launch_simt<__nv_bfloat16>(h, D.ops, n1, t1, st);
+            launch_simt<__nv_bfloat16>(h, D.ops + n1, (int)ops.size() - n1, t2, st);
+        }
+        return finish(h, D, st);
+    }
+
+    BwdCall c;
+    c.h = h; c.X = X; c.W = W; c.dY = dY; c.dX = dX; c.saved = saved;
+    c.P = std::move(P);
+    c.dY_in = dY_in;
+    c.ep = std::move(ep);
+    StageCopies cs{};
+    s = bwd_prepare(c, st, cs);
+    if (s != PLORA_OK) return s;
+    return bwd_launch(&c, 1, st, cs);
+}
+
+// ---------------------------------------------------------------------------
+// Muon
+// ---------------------------------------------------------------------------
+cudaError_t muon_setup() {
+    cudaError_t e = cudaFuncSetAttribute(muon_ns_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMuonNsSmem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(muon_apply_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 2 * PLORA_MAX_RANK * (kMuonApply + 1) * (int)sizeof(float));
+    return e;
+}
+
+struct MuonPlan {
+    std::vector<MuonMat> mats;   // work offsets in part, ns, Q until muon_bind
+    int64_t gram_blocks = 0, apply_blocks = 0;
+    int32_t smax = 1;
+    size_t bytes = 0;
+};
+
+// The matrices of the adapters' factors (one A and one B per output block), their blocks in each launch
+// and their places in the work buffer.  A matrix's split depends on its own shape alone.
+void muon_plan(const plora_ctx* h, int32_t n, const plora_adapter* tab, MuonPlan& P) {
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = o;
+        o = (size_t)round_up((int64_t)(o + bytes), 256);
+        return reinterpret_cast<uint8_t*>(0) + at;
+    };
+    auto add = [&](int64_t rows, int64_t cols) {
+        MuonMat M{};
+        M.tall = rows > cols;
+        M.s = (int32_t)std::min(rows, cols);
+        M.L = (int32_t)std::max(rows, cols);
+        M.nchunks = (int32_t)ceil_div(M.L, kMuonChunk);
+        const size_t n2 = (size_t)M.s * (size_t)M.s;
+        M.part = reinterpret_cast<double*>(take(n2 * (size_t)M.nchunks * sizeof(double)));
+        M.ns = reinterpret_cast<double*>(take(4 * n2 * sizeof(double)));
+        M.Q = reinterpret_cast<float*>(take((n2 + 1) * sizeof(float)));
+        const int64_t nt = ceil_div(M.s, kMuonTile);
+        M.gram0 = (int32_t)P.gram_blocks;
+        M.apply0 = (int32_t)P.apply_blocks;
+        P.gram_blocks += M.nchunks * (nt * (nt + 1) / 2);
+        P.apply_blocks += ceil_div(M.L, kMuonApply);
+        P.smax = std::max(P.smax, M.s);
+        P.mats.push_back(M);
+    };
+    for (int32_t i = 0; i < n; ++i) {
+        const int64_t r = tab[i].rank;
+        for (int b = 0; b < h->nblk; ++b) add(r, h->cfg.d_in);
+        for (int b = 0; b < h->nblk; ++b) add(h->blk_end[b] - (b ? h->blk_end[b - 1] : 0), r);
+    }
+    P.bytes = o;
+}
+
+plora_status muon_ranks(plora_ctx* h, int32_t n, const plora_adapter* tab) {
+    if (n < 0 || n > h->cfg.max_adapters)
+        return fail(h, PLORA_ERR_INVALID_ARG, "n_adapters=%d outside [0, max_adapters=%d]", n, h->cfg.max_adapters);
+    if (n > 0 && !tab) return fail(h, PLORA_ERR_INVALID_ARG, "adapter table is NULL");
+    for (int32_t i = 0; i < n; ++i)
+        if (tab[i].rank < 1 || tab[i].rank > h->cfg.max_rank)
+            return fail(h, PLORA_ERR_INVALID_ARG, "adapter %d: rank %d outside [1, max_rank=%d]", i, tab[i].rank,
+                        h->cfg.max_rank);
+    return PLORA_OK;
+}
+
+plora_status muon_step(plora_ctx* h, int32_t n, const plora_adapter* tab, const plora_muon_state* st, void* work,
+                       cudaStream_t cs) {
+    plora_status s = muon_ranks(h, n, tab);
+    if (s != PLORA_OK || n == 0) return s;
+    if (!st) return fail(h, PLORA_ERR_INVALID_ARG, "optimizer state is NULL");
+    if (!get_range_fn()) return fail(h, PLORA_ERR_CUDA, "cuMemGetAddressRange is not available");
+    const bool bf16 = h->cfg.dtype == PLORA_BF16;
+    const size_t di = (size_t)h->cfg.d_in, dout = (size_t)h->cfg.d_out;
+    std::vector<Span> spans;
+    for (int32_t i = 0; i < n; ++i) {
+        const plora_adapter& a = tab[i];
+        const plora_muon_state& o = st[i];
+        if (!(o.momentum >= 0.f && o.momentum < 1.f) || !(o.eps > 0.f) || !std::isfinite(o.eps) ||
+            !std::isfinite(o.lr) || !std::isfinite(o.weight_decay) || !std::isfinite(o.a) || !std::isfinite(o.b) ||
+            !std::isfinite(o.c) || o.ns_steps < 1 || o.ns_steps > PLORA_MUON_MAX_STEPS ||
+            (o.nesterov != 0 && o.nesterov != 1) || o.scale < PLORA_MUON_SCALE_NONE || o.scale > PLORA_MUON_SCALE_RMS ||
+            o.reserved != 0)
+            return fail(h, PLORA_ERR_INVALID_ARG, "adapter %d: invalid Muon hyper-parameters", i);
+        if (bf16 && (!o.A_master || !o.B_master))
+            return fail(h, PLORA_ERR_INVALID_ARG, "adapter %d: a bf16 handle needs fp32 master copies", i);
+        if (!bf16 && (o.A_master || o.B_master))
+            return fail(h, PLORA_ERR_INVALID_ARG, "adapter %d: an fp32 handle updates A and B in place", i);
+        const size_t na = (size_t)a.rank * (size_t)h->nblk * di, nb = dout * (size_t)a.rank;
+        const Span own[] = {
+            {reinterpret_cast<uintptr_t>(a.dA), na * 4, false}, {reinterpret_cast<uintptr_t>(a.dB), nb * 4, false},
+            {reinterpret_cast<uintptr_t>(o.mA), na * 4, true}, {reinterpret_cast<uintptr_t>(o.mB), nb * 4, true},
+            {reinterpret_cast<uintptr_t>(a.A), na * h->esize, true}, {reinterpret_cast<uintptr_t>(a.B), nb * h->esize, true},
+            {reinterpret_cast<uintptr_t>(o.A_master), na * 4, true}, {reinterpret_cast<uintptr_t>(o.B_master), nb * 4, true}};
+        for (int k = 0; k < (bf16 ? 8 : 6); ++k) {
+            const void* p = reinterpret_cast<const void*>(own[k].at);
+            if (!p || !aligned16(p))
+                return fail(h, PLORA_ERR_INVALID_ARG, "adapter %d: a parameter, gradient or state pointer is NULL "
+                            "or not 16-byte aligned", i);
+            if (!in_device_allocation(p, own[k].bytes))
+                return fail(h, PLORA_ERR_INVALID_ARG, "adapter %d: a parameter, gradient or state buffer is not a "
+                            "device buffer of its size", i);
+            spans.push_back(own[k]);
+        }
+    }
+    MuonPlan P;
+    muon_plan(h, n, tab, P);
+    if (P.gram_blocks > INT32_MAX || P.apply_blocks > INT32_MAX)
+        return fail(h, PLORA_ERR_UNSUPPORTED, "the step's launches exceed 2^31 blocks");
+    if (!work || (reinterpret_cast<uintptr_t>(work) & 255u) != 0 || !in_device_allocation(work, P.bytes))
+        return fail(h, PLORA_ERR_INVALID_ARG, "work is not a 256-byte aligned device buffer of %zu bytes", P.bytes);
+    spans.push_back(Span{reinterpret_cast<uintptr_t>(work), P.bytes, true});
+    if (spans_clash(spans))
+        return fail(h, PLORA_ERR_INVALID_ARG, "a buffer that the step writes overlaps another of its buffers");
+    DeviceGuard guard;
+    cudaError_t ce = guard.enter(h->device);
+    if (ce != cudaSuccess) return cuda_fail(h, ce, "cudaSetDevice");
+    size_t k = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        const plora_muon_state& o = st[i];
+        const int64_t r = tab[i].rank;
+        for (int side = 0; side < 2; ++side) {
+            int64_t at = 0;
+            for (int b = 0; b < h->nblk; ++b) {
+                MuonMat& M = P.mats[k++];
+                const int64_t width = h->blk_end[b] - (b ? h->blk_end[b - 1] : 0);
+                const int64_t rows = side ? width : r, cols = side ? r : (int64_t)di;
+                float* master = side ? o.B_master : o.A_master;
+                void* par = const_cast<void*>(side ? tab[i].B : tab[i].A);
+                M.g = (side ? tab[i].dB : tab[i].dA) + at;
+                M.m = (side ? o.mB : o.mA) + at;
+                M.p = (bf16 ? master : static_cast<float*>(par)) + at;
+                M.out = bf16 ? static_cast<__nv_bfloat16*>(par) + at : nullptr;
+                at += rows * cols;
+                uint8_t* w = static_cast<uint8_t*>(work);
+                M.part = reinterpret_cast<double*>(w + reinterpret_cast<uintptr_t>(M.part));
+                M.ns = reinterpret_cast<double*>(w + reinterpret_cast<uintptr_t>(M.ns));
+                M.Q = reinterpret_cast<float*>(w + reinterpret_cast<uintptr_t>(M.Q));
+                double shape = 1.0;
+                if (o.scale == PLORA_MUON_SCALE_ROWS) shape = std::sqrt(std::max(1.0, (double)rows / (double)cols));
+                if (o.scale == PLORA_MUON_SCALE_RMS) shape = 0.2 * std::sqrt((double)std::max(rows, cols));
+                M.mu = o.momentum;
+                M.decay = (float)(1.0 - (double)o.lr * (double)o.weight_decay);
+                M.step = (float)((double)o.lr * shape);
+                M.eps = o.eps;
+                M.a = o.a; M.b = o.b; M.c = o.c;
+                M.steps = o.ns_steps;
+                M.nesterov = o.nesterov;
+            }
+        }
+    }
+    uint8_t *dm = nullptr, *none = nullptr;
+    int slot = 0;
+    s = upload_parts(h, P.mats.data(), P.mats.size() * sizeof(MuonMat), nullptr, 0, cs, &dm, &none, &slot);
+    if (s != PLORA_OK) return s;
+    const MuonMat* mats = reinterpret_cast<const MuonMat*>(dm);
+    const int nm = (int)P.mats.size();
+    tracked(h, kMuonGramK, cs, [&] { muon_gram_kernel<<<(unsigned)P.gram_blocks, 256, 0, cs>>>(mats, nm); });
+    tracked(h, kMuonNsK, cs, [&] { muon_ns_kernel<<<(unsigned)nm * kMuonCluster, 256, kMuonNsSmem, cs>>>(mats); });
+    const size_t sm = 2 * (size_t)P.smax * (kMuonApply + 1) * sizeof(float);
+    tracked(h, kMuonApplyK, cs, [&] { muon_apply_kernel<<<(unsigned)P.apply_blocks, 256, sm, cs>>>(mats, nm); });
+    DevPlan D;
+    D.slot = slot;
+    return finish(h, D, cs);
 }
 
 }  // namespace
@@ -1290,13 +1805,17 @@ plora_status plora_create(plora_handle* out, const plora_config* cfg) {
                     (size_t)round_up(ops_max * (int64_t)sizeof(SimtOp), 256) +
                     (size_t)round_up((tok_max + 1) * (int64_t)sizeof(MTileRec), 256) +
                     (size_t)round_up((tok_max + na) * (int64_t)sizeof(LoraSeg), 256) +
-                    (size_t)round_up(kDynCounters * (int64_t)sizeof(int32_t), 256) + 1024;
+                    (size_t)round_up(kDynCounters * (int64_t)sizeof(int32_t), 256) +
+                    (size_t)round_up(na * (int64_t)sizeof(void*), 256) * 2 +          // epilogue tables
+                    (size_t)round_up(na * (int64_t)sizeof(int32_t), 256) + 1024;
     // The AdamW step's tables (segments and chunks) travel through the same staging ring.
     const int64_t adamw_chunks =
         2 * na + na * (int64_t)cfg->max_rank * (nblk * cfg->d_in + cfg->d_out) / kAdamwChunk;
     h->blob_bytes = std::max(h->blob_bytes, (size_t)round_up(2 * na * (int64_t)sizeof(AdamwSeg), 256) +
                                                 (size_t)round_up(adamw_chunks * (int64_t)sizeof(AdamwChunk), 256) +
                                                 1024);
+    // So does the Muon step's table, two matrices per adapter and output block.
+    h->blob_bytes = std::max(h->blob_bytes, (size_t)round_up(2 * na * nblk * (int64_t)sizeof(MuonMat), 256) + 1024);
 
     size_t o = 0;
     auto carve = [&](Region& r, size_t bytes) {
@@ -1322,6 +1841,7 @@ plora_status plora_create(plora_handle* out, const plora_config* cfg) {
     }
     if (e == cudaSuccess && h->tc) {
         e = set_tc_attr<Op::BaseFwd>();
+        if (e == cudaSuccess) e = (set_tc_attr<Op::BaseFwd, Op::BaseFwd, true>());
         if (e == cudaSuccess) e = set_tc_attr<Op::BaseDx>();
         if (e == cudaSuccess) e = set_tc_attr<Op::ShrinkX>();
         if (e == cudaSuccess) e = set_tc_attr<Op::ShrinkDy>();
@@ -1334,6 +1854,7 @@ plora_status plora_create(plora_handle* out, const plora_config* cfg) {
         if (e == cudaSuccess) e = pair_setup<Op::BaseFwd>(h->pairs_fwd);
         if (e == cudaSuccess) e = pair_setup<Op::BaseDx>(h->pairs_dx);
     }
+    if (e == cudaSuccess) e = muon_setup();
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -1420,115 +1941,68 @@ plora_status plora_saved_bytes(plora_handle h, int32_t n, const int64_t* off, co
 
 plora_status plora_forward(plora_handle h, const void* X, const void* W, void* Y, int32_t n, const int64_t* off,
                            const plora_adapter* tab, void* saved, void* stream) {
-    if (!h) return PLORA_ERR_INVALID_ARG;
-    h->last_error.clear();
-    HostPlan P;
-    plora_status s = fwd_args(h, X, W, Y, n, off, tab, saved, P);
-    if (s != PLORA_OK || P.T == 0) return s;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t d_in = h->cfg.d_in, d_out = h->cfg.d_out;
-
-    if (!h->tc) {
-        std::vector<SimtOp> ops;
-        int32_t t1 = 0, t2 = 0;
-        const bool f32 = h->cfg.dtype == PLORA_FP32;
-        const size_t es = h->esize;
-        // K1: Y = X W.  K2: H'_i = s_i X_i A_i.
-        add_op(ops, t1, X, d_in, 1, W, 1, d_in, Y, d_out, 1, P.T, d_out, d_in, 1.f, false, f32);
-        for (const AdapterDev& a : P.ad) {
-            if (a.n == 0) continue;
-            add_op(ops, t1, (const uint8_t*)X + (size_t)a.x_row * d_in * es, d_in, 1, a.A, 1, d_in,
-                   (uint8_t*)saved + (size_t)a.h_row * P.RP * es, P.RP, 1, a.n, a.rank, d_in, a.scale, false, f32);
-        }
-        const int n1 = (int)ops.size();
-        // K3: Y_i += H'_i B_i.
-        for (const AdapterDev& a : P.ad) {
-            if (a.n == 0) continue;
-            add_op(ops, t2, (const uint8_t*)saved + (size_t)a.h_row * P.RP * es, P.RP, 1, a.B, 1, a.rank,
-                   (uint8_t*)Y + (size_t)a.x_row * d_out * es, d_out, 1, a.n, d_out, a.rank, 1.f, true, f32);
-        }
-        DevPlan D;
-        s = upload(h, P, ops, st, D);
-        if (s != PLORA_OK) return s;
-        if (f32) {
-            launch_simt<float>(h, D.ops, n1, t1, st);
-            launch_simt<float>(h, D.ops + n1, (int)ops.size() - n1, t2, st);
-        } else {
-            launch_simt<__nv_bfloat16>(h, D.ops, n1, t1, st);
-            launch_simt<__nv_bfloat16>(h, D.ops + n1, (int)ops.size() - n1, t2, st);
-        }
-        return finish(h, D, st);
-    }
-
-    // Tensor-core path.
-    FwdCall c;
-    c.h = h; c.X = X; c.W = W; c.Y = Y; c.saved = saved;
-    c.P = std::move(P);
-    StageCopies cs{};
-    s = fwd_prepare(c, st, cs);
-    if (s != PLORA_OK) return s;
-    return fwd_launch(&c, 1, st, cs);
+    return forward_call(h, X, W, Y, n, off, tab, saved, nullptr, stream);
 }
 
 plora_status plora_backward(plora_handle h, const void* X, const void* W, const void* dY, void* dX, int32_t n,
                             const int64_t* off, const plora_adapter* tab, const void* saved, void* stream) {
+    return backward_call(h, X, W, dY, dX, n, off, tab, saved, nullptr, stream);
+}
+plora_status plora_epilogue_work_bytes(plora_handle h, int32_t n, const int64_t* off, const plora_epilogue* ep,
+                                       size_t* bytes) {
     if (!h) return PLORA_ERR_INVALID_ARG;
     h->last_error.clear();
-    HostPlan P;
-    plora_status s = bwd_args(h, X, W, dY, dX, n, off, tab, saved, P);
+    if (!bytes) return fail(h, PLORA_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = 0;
+    if (!ep) return fail(h, PLORA_ERR_INVALID_ARG, "the epilogue is NULL");
+    if (ep->activation < PLORA_ACT_NONE || ep->activation > PLORA_ACT_SILU || ep->reserved != 0)
+        return fail(h, PLORA_ERR_INVALID_ARG, "activation=%d, reserved=%d", ep->activation, ep->reserved);
+    const plora_status s = check_offsets(h, n, off);
     if (s != PLORA_OK) return s;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t d_in = h->cfg.d_in, d_out = h->cfg.d_out;
-    s = zero_empty_grads(h, P, tab, st);
-    if (s != PLORA_OK || P.T == 0) return s;
-    void* G = h->at<void>(h->r_G);
-
-    if (!h->tc) {
-        std::vector<SimtOp> ops;
-        int32_t t1 = 0, t2 = 0;
-        const bool f32 = h->cfg.dtype == PLORA_FP32;
-        const size_t es = h->esize;
-        // Phase 1 -- K4: dX = dY W^T; K5: G_i = s_i dY_i B_i^T; K7: dB_i = dY_i^T H'_i.
-        if (dX) add_op(ops, t1, dY, d_out, 1, W, d_in, 1, dX, d_in, 1, P.T, d_in, d_out, 1.f, false, f32);
-        for (const AdapterDev& a : P.ad) {
-            if (a.n == 0) continue;
-            add_op(ops, t1, (const uint8_t*)dY + (size_t)a.x_row * d_out * es, d_out, 1, a.B, a.rank, 1,
-                   (uint8_t*)G + (size_t)a.h_row * P.RP * es, P.RP, 1, a.n, a.rank, d_out, a.scale, false, f32);
-            add_op(ops, t1, (const uint8_t*)dY + (size_t)a.x_row * d_out * es, 1, d_out,
-                   (const uint8_t*)saved + (size_t)a.h_row * P.RP * es, P.RP, 1, a.dB, a.rank, 1, d_out, a.rank,
-                   a.n, 1.f, false, true);
-        }
-        const int n1 = (int)ops.size();
-        // Phase 2 -- K6: dX_i += G_i A_i^T; K8: dA_i = X_i^T G_i.
-        for (const AdapterDev& a : P.ad) {
-            if (a.n == 0) continue;
-            if (dX)
-                add_op(ops, t2, (const uint8_t*)G + (size_t)a.h_row * P.RP * es, P.RP, 1, a.A, d_in, 1,
-                       (uint8_t*)dX + (size_t)a.x_row * d_in * es, d_in, 1, a.n, d_in, a.rank, 1.f, true, f32);
-            add_op(ops, t2, (const uint8_t*)X + (size_t)a.x_row * d_in * es, 1, d_in,
-                   (const uint8_t*)G + (size_t)a.h_row * P.RP * es, P.RP, 1, a.dA, 1, d_in, d_in, a.rank, a.n,
-                   1.f, false, true);
-        }
-        DevPlan D;
-        s = upload(h, P, ops, st, D);
-        if (s != PLORA_OK) return s;
-        if (f32) {
-            launch_simt<float>(h, D.ops, n1, t1, st);
-            launch_simt<float>(h, D.ops + n1, (int)ops.size() - n1, t2, st);
-        } else {
-            launch_simt<__nv_bfloat16>(h, D.ops, n1, t1, st);
-            launch_simt<__nv_bfloat16>(h, D.ops + n1, (int)ops.size() - n1, t2, st);
-        }
-        return finish(h, D, st);
+    int64_t tiles = 0;
+    bool db = false;
+    for (int32_t i = 0; i < n; ++i) {
+        tiles += ceil_div(off[i + 1] - off[i], kTileM);
+        db = db || (ep->dbias && ep->dbias[i]);
     }
+    *bytes = epi_work(h, off[n], tiles, ep->activation != PLORA_ACT_NONE, db).bytes;
+    return PLORA_OK;
+}
 
-    BwdCall c;
-    c.h = h; c.X = X; c.W = W; c.dY = dY; c.dX = dX; c.saved = saved;
-    c.P = std::move(P);
-    StageCopies cs{};
-    s = bwd_prepare(c, st, cs);
-    if (s != PLORA_OK) return s;
-    return bwd_launch(&c, 1, st, cs);
+plora_status plora_forward_epilogue(plora_handle h, const void* X, const void* W, void* Y, int32_t n,
+                                    const int64_t* off, const plora_adapter* tab, void* saved,
+                                    const plora_epilogue* ep, void* stream) {
+    if (!h) return PLORA_ERR_INVALID_ARG;
+    if (!ep) {
+        h->last_error.clear();
+        return fail(h, PLORA_ERR_INVALID_ARG, "the epilogue is NULL");
+    }
+    DeviceGuard guard;
+    const cudaError_t ge = guard.enter(h->device);
+    if (ge != cudaSuccess) return cuda_fail(h, ge, "cudaSetDevice");
+    try {
+        return forward_call(h, X, W, Y, n, off, tab, saved, ep, stream);
+    } catch (const std::bad_alloc&) {
+        return fail(h, PLORA_ERR_OOM, "out of host memory");
+    }
+}
+
+plora_status plora_backward_epilogue(plora_handle h, const void* X, const void* W, const void* dY, void* dX, int32_t n,
+                                     const int64_t* off, const plora_adapter* tab, const void* saved,
+                                     const plora_epilogue* ep, void* stream) {
+    if (!h) return PLORA_ERR_INVALID_ARG;
+    if (!ep) {
+        h->last_error.clear();
+        return fail(h, PLORA_ERR_INVALID_ARG, "the epilogue is NULL");
+    }
+    DeviceGuard guard;
+    const cudaError_t ge = guard.enter(h->device);
+    if (ge != cudaSuccess) return cuda_fail(h, ge, "cudaSetDevice");
+    try {
+        return backward_call(h, X, W, dY, dX, n, off, tab, saved, ep, stream);
+    } catch (const std::bad_alloc&) {
+        return fail(h, PLORA_ERR_OOM, "out of host memory");
+    }
 }
 
 plora_status plora_device_info(plora_handle h, int32_t* out, int32_t capacity, int32_t* count) {
@@ -1669,6 +2143,34 @@ plora_status plora_adamw_step(plora_handle h, int32_t n, const plora_adapter* ta
     DevPlan D;
     D.slot = slot;
     return finish(h, D, cs);
+}
+
+plora_status plora_muon_work_bytes(plora_handle h, int32_t n, const plora_adapter* tab, size_t* bytes) {
+    if (!h) return PLORA_ERR_INVALID_ARG;
+    h->last_error.clear();
+    if (!bytes) return fail(h, PLORA_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = 0;
+    try {
+        const plora_status s = muon_ranks(h, n, tab);
+        if (s != PLORA_OK) return s;
+        MuonPlan P;
+        muon_plan(h, n, tab, P);
+        *bytes = P.bytes;
+        return PLORA_OK;
+    } catch (const std::bad_alloc&) {
+        return fail(h, PLORA_ERR_OOM, "out of host memory");
+    }
+}
+
+plora_status plora_muon_step(plora_handle h, int32_t n, const plora_adapter* tab, const plora_muon_state* st,
+                             void* work, void* stream) {
+    if (!h) return PLORA_ERR_INVALID_ARG;
+    h->last_error.clear();
+    try {
+        return muon_step(h, n, tab, st, work, static_cast<cudaStream_t>(stream));
+    } catch (const std::bad_alloc&) {
+        return fail(h, PLORA_ERR_OOM, "out of host memory");
+    }
 }
 
 plora_status plora_debug_timeout_probe(plora_handle h, int64_t timeout_ns, void* stream) {

@@ -45,6 +45,7 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include "epilogue.cuh"
 #include "plan.cuh"
 #include "ptx.cuh"
 
@@ -644,6 +645,115 @@ __device__ __forceinline__ void epilogue_store_tma(const CUtensorMap* tmC, uint3
     }
 }
 
+// The projection's own epilogue in a launch of one base GEMM: Z = accumulator + bias, Y = act(Z) + residual.
+struct EpiFused {
+    int32_t act;
+    int32_t want_z;              // Z is written too (through the map in slot m[1][0])
+    const void* const* bias;     // [n] device pointers (entries may be null), or null
+    const __nv_bfloat16* residual;   // [M][N] or null
+};
+
+// This thread's bias row: the bias of the adapter that owns output row `row` (null: no bias).  rec is
+// the overlap record of the row's 256-row block.
+__device__ __forceinline__ const __nv_bfloat16* bias_of_row(const TcParams& p, const EpiFused& ep, const MTileRec& rec,
+                                                            int row) {
+    if (!ep.bias) return nullptr;
+    for (int q = rec.q0; q < rec.q1; ++q) {
+        const int i = mtile_seg(p, rec, q).adapter;
+        if (!dcheck(p.err_flag, i >= 0 && i < p.n_adapters)) continue;
+        const int x0 = p.adapters[i].x_row;
+        if (row >= x0 && row < x0 + p.adapters[i].n) return static_cast<const __nv_bfloat16*>(ep.bias[i]);
+    }
+    return nullptr;
+}
+
+// epilogue_store_tma with the projection's epilogue.  The bias, the activation and the residual are
+// applied to the fp32 accumulator, so Y and Z are each rounded once.  A lane owns one output row: its
+// bias loads hit the same line in every lane whose row has the same adapter, and its residual loads
+// (requested before the accumulator is read) take whole 128-byte lines over a 64-column chunk.
+__device__ __forceinline__ void epilogue_store_ep(const CUtensorMap* tmY, const CUtensorMap* tmZ, uint32_t t_row,
+                                                  uint8_t* wbuf, int lane, int row0, int n0, int M_total, int N_total,
+                                                  const EpiFused& ep, const __nv_bfloat16* bias, uint32_t& seq) {
+    if (row0 >= M_total) return;
+    const uint32_t sw = (uint32_t)(lane & 7);
+    const bool row_ok = row0 + lane < M_total;
+    const __nv_bfloat16* res = ep.residual && row_ok ? ep.residual + (int64_t)(row0 + lane) * N_total : nullptr;
+    // writes the 64 values v as one swizzled 32 x 64 box and stores it through map tm
+    auto put = [&](const CUtensorMap* tm, const float (&v)[64], int col0) {
+        uint8_t* buf = wbuf + (seq++ & 1u) * kEpiBufBytes;
+        if (lane == 0) ptx::bulk_wait_read<1>();   // the store that last read this buffer is done
+        __syncwarp();
+        const uint32_t rowaddr = ptx::smem_u32(buf) + (uint32_t)lane * 128u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint4 o;
+            o.x = pack_bf16x2(v[8 * j], v[8 * j + 1]);
+            o.y = pack_bf16x2(v[8 * j + 2], v[8 * j + 3]);
+            o.z = pack_bf16x2(v[8 * j + 4], v[8 * j + 5]);
+            o.w = pack_bf16x2(v[8 * j + 6], v[8 * j + 7]);
+            ptx::st_shared_v4(rowaddr + ((((uint32_t)j) ^ sw) << 4), o);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            ptx::tma_store_2d(tm, buf, col0, row0);
+            ptx::bulk_commit();
+        }
+    };
+    for (int ch = 0; ch < kTileN / 64; ++ch) {
+        const int col0 = n0 + ch * 64;
+        if (col0 >= N_total) break;
+        uint4 rv[8];
+        if (res) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (col0 + 8 * j < N_total) rv[j] = *reinterpret_cast<const uint4*>(res + col0 + 8 * j);
+        }
+        __syncwarp();
+        float z[64];
+        {
+            uint32_t ra[32], rb[32];
+            ptx::tmem_ld32(t_row + ch * 64, ra);
+            ptx::tmem_ld32(t_row + ch * 64 + 32, rb);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                z[k] = __uint_as_float(ra[k]);
+                z[32 + k] = __uint_as_float(rb[k]);
+            }
+        }
+        if (bias) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (col0 + 8 * j >= N_total) continue;
+                float b[8];
+                load8<__nv_bfloat16>(bias + col0 + 8 * j, b);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) z[8 * j + k] += b[k];
+            }
+        }
+        if (ep.want_z) put(tmZ, z, col0);
+        with_act(ep.act, [&](auto ACT) {
+#pragma unroll
+            for (int k = 0; k < 64; ++k) z[k] = act_fwd<ACT.value>(z[k]);
+        });
+        if (res) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (col0 + 8 * j >= N_total) continue;
+                const uint32_t w[4] = {rv[j].x, rv[j].y, rv[j].z, rv[j].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = unpack_bf16x2(w[k]);
+                    z[8 * j + 2 * k] += f.x;
+                    z[8 * j + 2 * k + 1] += f.y;
+                }
+            }
+        }
+        put(tmY, z, col0);
+    }
+}
+
 // Epilogue (warps 2..5, one accumulator row per thread): drains work item ti's accumulator
 // rows from TMEM at t_row and runs the op's output step.
 template <Op OP>
@@ -880,6 +990,7 @@ struct GroupParams {
     // With a second op, a counter that starts at zero (the call's schedule copy clears it): its items
     // are then claimed one at a time (nullptr: every item dealt round-robin).
     int32_t* dyn;
+    EpiFused ep;                   // EP launches (one segment): the projection's epilogue
     TcParams p[kMaxSeg];
 };
 constexpr int kItemQ = 4;   // item queue slots (producer -> MMA and epilogue roles) for claimed items
@@ -887,10 +998,12 @@ struct GroupMaps {
     CUtensorMap m[kMaxSeg][5];
 };
 
-template <Op OP, Op OP2 = OP>
+// EP: the launch is one base GEMM (segment 0) with the projection's epilogue g.ep; m[1][0] is Z's map.
+template <Op OP, Op OP2 = OP, bool EP = false>
 __global__ void __launch_bounds__(kTcThreads, 1)
 tc_kernel(const __grid_constant__ GroupMaps maps, const __grid_constant__ GroupParams g) {
     using Tr = OpTraits<OP>;
+    static_assert(!EP || (OP == Op::BaseFwd && Tr::kWide), "the fused epilogue is the 256-row forward tile's");
     static_assert(OP2 == OP || !OpTraits<OP2>::kBase, "the second op of a launch is not a base GEMM");
     const TcParams& p0 = g.p[0];
     const int total = g.begin[g.n_seg];
@@ -1101,8 +1214,14 @@ tc_kernel(const __grid_constant__ GroupMaps maps, const __grid_constant__ GroupP
                         }
                         ptx::tc_fence_after();
                         const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kTileN);
-                        epilogue_store_tma(&maps.m[j][4], t_row, wbuf, lane, ti.out_row + h * kTileM + q * 32, ti.n0,
-                                           pj.M_total, pj.N_total, epi_seq);
+                        const int row0 = ti.out_row + h * kTileM + q * 32;
+                        if constexpr (EP)
+                            epilogue_store_ep(&maps.m[j][4], &maps.m[1][0], t_row, wbuf, lane, row0, ti.n0, pj.M_total,
+                                              pj.N_total, g.ep, bias_of_row(pj, g.ep, pj.mt_rec[ti.mtile], row0 + lane),
+                                              epi_seq);
+                        else
+                            epilogue_store_tma(&maps.m[j][4], t_row, wbuf, lane, row0, ti.n0, pj.M_total, pj.N_total,
+                                               epi_seq);
                         ptx::tc_fence_before();
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(&acce_bar[b]);
