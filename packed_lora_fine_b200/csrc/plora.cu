@@ -1550,53 +1550,83 @@ plora_status backward_call(plora_ctx* h, const void* X, const void* W, const voi
 // Muon
 // ---------------------------------------------------------------------------
 cudaError_t muon_setup() {
-    cudaError_t e = cudaFuncSetAttribute(muon_ns_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMuonNsSmem);
+    cudaError_t e = cudaFuncSetAttribute(muon_gram_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGramSmem);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(muon_apply_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 2 * PLORA_MAX_RANK * (kMuonApply + 1) * (int)sizeof(float));
+        e = cudaFuncSetAttribute(muon_ns_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMuonNsSmem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(muon_apply_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kApplySmem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(muon_apply_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kApplySmem);
     return e;
 }
 
+// One matrix of a step before its pointers are known: where it is in the adapters' tensors and in the work
+// buffer.
+struct MuonPlace {
+    int32_t adapter, side;       // side 0: A, 1: B
+    int64_t at, rows, cols;      // its first element in the adapter's tensor, and its shape
+    size_t part, ns, q, hdr;     // byte offsets in the work buffer
+};
+
 struct MuonPlan {
-    std::vector<MuonMat> mats;   // work offsets in part, ns, Q until muon_bind
-    int64_t gram_blocks = 0, apply_blocks = 0;
-    int32_t smax = 1;
+    std::vector<MuonMat> mats;   // those with s <= kMuonBigS first
+    std::vector<MuonPlace> place;
+    int32_t n_small = 0;
+    int64_t gram_items = 0;
+    int64_t tiles[2] = {};       // apply tiles of the small and of the big ones
     size_t bytes = 0;
 };
 
-// The matrices of the adapters' factors (one A and one B per output block), their blocks in each launch
+// The matrices of the adapters' factors (one A and one B per output block), their items in each launch
 // and their places in the work buffer.  A matrix's split depends on its own shape alone.
 void muon_plan(const plora_ctx* h, int32_t n, const plora_adapter* tab, MuonPlan& P) {
-    size_t o = 0;
     auto take = [&](size_t bytes) {
-        const size_t at = o;
-        o = (size_t)round_up((int64_t)(o + bytes), 256);
-        return reinterpret_cast<uint8_t*>(0) + at;
+        const size_t at = P.bytes;
+        P.bytes = (size_t)round_up((int64_t)(P.bytes + bytes), 256);
+        return at;
     };
-    auto add = [&](int64_t rows, int64_t cols) {
-        MuonMat M{};
-        M.tall = rows > cols;
-        M.s = (int32_t)std::min(rows, cols);
-        M.L = (int32_t)std::max(rows, cols);
-        M.nchunks = (int32_t)ceil_div(M.L, kMuonChunk);
-        const size_t n2 = (size_t)M.s * (size_t)M.s;
-        M.part = reinterpret_cast<double*>(take(n2 * (size_t)M.nchunks * sizeof(double)));
-        M.ns = reinterpret_cast<double*>(take(4 * n2 * sizeof(double)));
-        M.Q = reinterpret_cast<float*>(take((n2 + 1) * sizeof(float)));
-        const int64_t nt = ceil_div(M.s, kMuonTile);
-        M.gram0 = (int32_t)P.gram_blocks;
-        M.apply0 = (int32_t)P.apply_blocks;
-        P.gram_blocks += M.nchunks * (nt * (nt + 1) / 2);
-        P.apply_blocks += ceil_div(M.L, kMuonApply);
-        P.smax = std::max(P.smax, M.s);
-        P.mats.push_back(M);
-    };
+    std::vector<MuonPlace> all;
     for (int32_t i = 0; i < n; ++i) {
         const int64_t r = tab[i].rank;
-        for (int b = 0; b < h->nblk; ++b) add(r, h->cfg.d_in);
-        for (int b = 0; b < h->nblk; ++b) add(h->blk_end[b] - (b ? h->blk_end[b - 1] : 0), r);
+        for (int side = 0; side < 2; ++side) {
+            int64_t at = 0;
+            for (int b = 0; b < h->nblk; ++b) {
+                MuonPlace p{};
+                p.adapter = i;
+                p.side = side;
+                p.at = at;
+                p.rows = side ? h->blk_end[b] - (b ? h->blk_end[b - 1] : 0) : r;
+                p.cols = side ? r : h->cfg.d_in;
+                at += p.rows * p.cols;
+                all.push_back(p);
+            }
+        }
     }
-    P.bytes = o;
+    for (int big = 0; big < 2; ++big)
+        for (MuonPlace p : all) {
+            MuonMat M{};
+            M.s = (int32_t)std::min(p.rows, p.cols);
+            M.L = (int32_t)std::max(p.rows, p.cols);
+            if ((M.s > kMuonBigS) != (big != 0)) continue;
+            M.tall = p.rows > p.cols;
+            M.J = M.s <= 64 ? 128 / M.s : 1;
+            M.tiles = (int32_t)ceil_div(M.L, (int64_t)kMuonTileL * M.J);
+            M.nchunks = (int32_t)ceil_div(M.tiles, kMuonGramTiles);
+            const int32_t ng = (int32_t)ceil_div(M.s, 64);
+            M.npairs = ng <= 2 ? 1 : ng * (ng - 1) / 2;
+            const size_t s2 = (size_t)M.s * (size_t)M.s, sp = (size_t)round_up(M.s, 8);
+            p.part = take(s2 * (size_t)M.nchunks * sizeof(double));
+            p.ns = take(4 * sp * sp * sizeof(double));
+            p.q = take((size_t)(big ? 24 : 6) * kMuonPlane);
+            p.hdr = take((size_t)(2 + M.nchunks * M.npairs + kMuonCluster) * sizeof(float));
+            M.gram0 = (int32_t)P.gram_items;
+            M.apply0 = (int32_t)P.tiles[big];
+            P.gram_items += M.nchunks * M.npairs;
+            P.tiles[big] += M.tiles;
+            P.n_small += big ? 0 : 1;
+            P.mats.push_back(M);
+            P.place.push_back(p);
+        }
 }
 
 plora_status muon_ranks(plora_ctx* h, int32_t n, const plora_adapter* tab) {
@@ -1651,8 +1681,8 @@ plora_status muon_step(plora_ctx* h, int32_t n, const plora_adapter* tab, const 
     }
     MuonPlan P;
     muon_plan(h, n, tab, P);
-    if (P.gram_blocks > INT32_MAX || P.apply_blocks > INT32_MAX)
-        return fail(h, PLORA_ERR_UNSUPPORTED, "the step's launches exceed 2^31 blocks");
+    if (P.gram_items > INT32_MAX || P.tiles[0] > INT32_MAX || P.tiles[1] > INT32_MAX)
+        return fail(h, PLORA_ERR_UNSUPPORTED, "the step has more than 2^31 tiles");
     if (!work || (reinterpret_cast<uintptr_t>(work) & 255u) != 0 || !in_device_allocation(work, P.bytes))
         return fail(h, PLORA_ERR_INVALID_ARG, "work is not a 256-byte aligned device buffer of %zu bytes", P.bytes);
     spans.push_back(Span{reinterpret_cast<uintptr_t>(work), P.bytes, true});
@@ -1661,39 +1691,31 @@ plora_status muon_step(plora_ctx* h, int32_t n, const plora_adapter* tab, const 
     DeviceGuard guard;
     cudaError_t ce = guard.enter(h->device);
     if (ce != cudaSuccess) return cuda_fail(h, ce, "cudaSetDevice");
-    size_t k = 0;
-    for (int32_t i = 0; i < n; ++i) {
-        const plora_muon_state& o = st[i];
-        const int64_t r = tab[i].rank;
-        for (int side = 0; side < 2; ++side) {
-            int64_t at = 0;
-            for (int b = 0; b < h->nblk; ++b) {
-                MuonMat& M = P.mats[k++];
-                const int64_t width = h->blk_end[b] - (b ? h->blk_end[b - 1] : 0);
-                const int64_t rows = side ? width : r, cols = side ? r : (int64_t)di;
-                float* master = side ? o.B_master : o.A_master;
-                void* par = const_cast<void*>(side ? tab[i].B : tab[i].A);
-                M.g = (side ? tab[i].dB : tab[i].dA) + at;
-                M.m = (side ? o.mB : o.mA) + at;
-                M.p = (bf16 ? master : static_cast<float*>(par)) + at;
-                M.out = bf16 ? static_cast<__nv_bfloat16*>(par) + at : nullptr;
-                at += rows * cols;
-                uint8_t* w = static_cast<uint8_t*>(work);
-                M.part = reinterpret_cast<double*>(w + reinterpret_cast<uintptr_t>(M.part));
-                M.ns = reinterpret_cast<double*>(w + reinterpret_cast<uintptr_t>(M.ns));
-                M.Q = reinterpret_cast<float*>(w + reinterpret_cast<uintptr_t>(M.Q));
-                double shape = 1.0;
-                if (o.scale == PLORA_MUON_SCALE_ROWS) shape = std::sqrt(std::max(1.0, (double)rows / (double)cols));
-                if (o.scale == PLORA_MUON_SCALE_RMS) shape = 0.2 * std::sqrt((double)std::max(rows, cols));
-                M.mu = o.momentum;
-                M.decay = (float)(1.0 - (double)o.lr * (double)o.weight_decay);
-                M.step = (float)((double)o.lr * shape);
-                M.eps = o.eps;
-                M.a = o.a; M.b = o.b; M.c = o.c;
-                M.steps = o.ns_steps;
-                M.nesterov = o.nesterov;
-            }
-        }
+    for (size_t k = 0; k < P.mats.size(); ++k) {
+        MuonMat& M = P.mats[k];
+        const MuonPlace& p = P.place[k];
+        const plora_adapter& a = tab[p.adapter];
+        const plora_muon_state& o = st[p.adapter];
+        void* par = const_cast<void*>(p.side ? a.B : a.A);
+        M.g = (p.side ? a.dB : a.dA) + p.at;
+        M.m = (p.side ? o.mB : o.mA) + p.at;
+        M.p = (bf16 ? (p.side ? o.B_master : o.A_master) : static_cast<float*>(par)) + p.at;
+        M.out = bf16 ? static_cast<__nv_bfloat16*>(par) + p.at : nullptr;
+        uint8_t* w = static_cast<uint8_t*>(work);
+        M.part = reinterpret_cast<double*>(w + p.part);
+        M.ns = reinterpret_cast<double*>(w + p.ns);
+        M.q = w + p.q;
+        M.hdr = reinterpret_cast<float*>(w + p.hdr);
+        double shape = 1.0;
+        if (o.scale == PLORA_MUON_SCALE_ROWS) shape = std::sqrt(std::max(1.0, (double)p.rows / (double)p.cols));
+        if (o.scale == PLORA_MUON_SCALE_RMS) shape = 0.2 * std::sqrt((double)std::max(p.rows, p.cols));
+        M.mu = o.momentum;
+        M.decay = (float)(1.0 - (double)o.lr * (double)o.weight_decay);
+        M.step = (float)((double)o.lr * shape);
+        M.eps = o.eps;
+        M.a = o.a; M.b = o.b; M.c = o.c;
+        M.steps = o.ns_steps;
+        M.nesterov = o.nesterov;
     }
     uint8_t *dm = nullptr, *none = nullptr;
     int slot = 0;
@@ -1701,10 +1723,24 @@ plora_status muon_step(plora_ctx* h, int32_t n, const plora_adapter* tab, const 
     if (s != PLORA_OK) return s;
     const MuonMat* mats = reinterpret_cast<const MuonMat*>(dm);
     const int nm = (int)P.mats.size();
-    tracked(h, kMuonGramK, cs, [&] { muon_gram_kernel<<<(unsigned)P.gram_blocks, 256, 0, cs>>>(mats, nm); });
+    int* err = h->at<int>(h->r_err);
+    tracked(h, kMuonGramK, cs, [&] {
+        muon_gram_kernel<<<(unsigned)P.gram_items, kGramThreads, kGramSmem, cs>>>(mats, nm, err, kTimeoutNs);
+    });
     tracked(h, kMuonNsK, cs, [&] { muon_ns_kernel<<<(unsigned)nm * kMuonCluster, 256, kMuonNsSmem, cs>>>(mats); });
-    const size_t sm = 2 * (size_t)P.smax * (kMuonApply + 1) * sizeof(float);
-    tracked(h, kMuonApplyK, cs, [&] { muon_apply_kernel<<<(unsigned)P.apply_blocks, 256, sm, cs>>>(mats, nm); });
+    const int32_t ns = P.n_small;
+    if (ns > 0)
+        tracked(h, kMuonApplyK, cs, [&] {
+            const int tiles = (int)P.tiles[0];
+            muon_apply_kernel<false><<<std::min(tiles, h->num_sms), kApplyThreads, kApplySmem, cs>>>(mats, 0, ns, tiles, err,
+                                                                                                  kTimeoutNs);
+        });
+    if (nm > ns)
+        tracked(h, kMuonApplyK, cs, [&] {
+            const int tiles = (int)P.tiles[1];
+            muon_apply_kernel<true><<<std::min(tiles, h->num_sms), kApplyThreads, kApplySmem, cs>>>(mats, ns, nm, tiles, err,
+                                                                                                 kTimeoutNs);
+        });
     DevPlan D;
     D.slot = slot;
     return finish(h, D, cs);
