@@ -39,7 +39,6 @@
 namespace plora {
 
 constexpr int kMuonTileL = 64;        // columns l' of a tile
-constexpr int kMuonGramTiles = 16;    // tiles of one Gram item
 constexpr int kMuonPlane = 128 * kMuonTileL * 2;   // bytes of one fp16 part of a tile (16 KB)
 constexpr int kMuonNsTile = 32;       // product tile of the iteration
 constexpr int kMuonCluster = 8;       // blocks per matrix in the iteration
@@ -52,7 +51,7 @@ struct MuonMat {
     float* p;
     __nv_bfloat16* out;   // the layer's bf16 copy, or nullptr when p is the parameter
     double* part;         // [nchunks][s][s] Gram partials
-    double* ns;           // four [sp][sp] matrices of the iteration, sp = s rounded up to 8
+    double* ns;           // five [sp][sp] matrices of the iteration, sp = s rounded up to 8 (s > 64)
     uint8_t* q;           // Q's fp16 parts as the apply pass stages them (muon_q_at)
     float* hdr;           // x scale, output scale, max|u| of each Gram item, max|Q| of each block
     int32_t s, L;
@@ -60,7 +59,8 @@ struct MuonMat {
     int32_t steps;
     int32_t J;            // long-side blocks stacked in a tile's rows (1 for s > 64)
     int32_t tiles;        // tiles of 64 J long-side indices
-    int32_t nchunks, npairs;   // Gram items: chunks of kMuonGramTiles tiles x pairs of 64-row groups
+    int32_t nchunks, npairs;   // Gram items: chunks of per_chunk tiles x pairs of 64-row groups
+    int32_t per_chunk, pad_;
     int32_t gram0;        // first item of this matrix in the Gram launch
     int32_t apply0;       // first tile in its apply launch
     float mu, decay;      // decay = 1 - lr wd
@@ -90,77 +90,255 @@ template <typename F> __device__ __forceinline__ int muon_find(int lo, int hi, i
     return lo;
 }
 
-// Four consecutive elements of a tile: `e` the first one's index in the matrix, n (0..4) how many exist.
-struct MuonQuad {
-    int32_t e;            // (a matrix has at most 65536 x 256 elements)
-    int n;
-};
-// Quad (row, x): row m and columns 4x.. of a tile if !tall, column l' = row and rows 4x.. if tall.  lo64,
-// hi64: the short-side index of tile rows 0 and 64 (0 and 64, or a pair of 64-row groups).
-__device__ __forceinline__ MuonQuad muon_quad(const MuonMat& M, int tile, int row, int x, int lo64, int hi64) {
-    MuonQuad q{0, 0};
-    if (!M.tall) {
-        int c, l = tile * kMuonTileL * M.J + 4 * x;
-        if (M.J > 1) {
-            const int j = row / M.s;
-            if (j >= M.J) return q;
-            c = row - j * M.s;
-            l += j * kMuonTileL;
-        } else {
-            c = row + (row < 64 ? lo64 : hi64 - 64);
-            if (c >= M.s) return q;
-        }
-        q.n = min(4, M.L - l);
-        q.e = c * M.L + l;
-    } else if (M.J > 1) {
-        const int w = M.J * M.s, m = 4 * x;
-        q.e = (tile * kMuonTileL + row) * w + m;
-        q.n = min(min(4, w - m), M.L * M.s - q.e);
-    } else {
-        const int l = tile * kMuonTileL + row, c = 4 * x + (4 * x < 64 ? lo64 : hi64 - 64);
-        if (l >= M.L) return q;
-        q.n = min(4, M.s - c);
-        q.e = l * M.s + c;
-    }
-    if (q.n < 0) q.n = 0;
-    return q;
-}
-// Whether every quad of the matrix starts at a multiple of four elements and is whole or empty.
-__device__ __forceinline__ bool muon_aligned(const MuonMat& M) {
-    return ((M.tall ? M.J * M.s : M.L) & 3) == 0;
-}
-__device__ __forceinline__ void muon_load4(const float* p, const MuonQuad& q, bool vec, float (&v)[4]) {
-    if (vec && q.n == 4) {
-        const float4 f = *reinterpret_cast<const float4*>(p + q.e);
-        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = k < q.n ? p[q.e + k] : 0.f;
-    }
+// Byte offset of element (row, y) in one part of a tile, 128-byte swizzled: rows of 64 elements (y < 64);
+// in a tall matrix's tile the row is the column l' and y the row m, in 64-row groups of 64 columns each.
+__device__ __forceinline__ uint32_t muon_elem_at(int row, int y) {
+    return (uint32_t)(y >> 6) * 8192u + (uint32_t)row * 128u + ((((uint32_t)y >> 3 & 7u) ^ ((uint32_t)row & 7u)) << 4) +
+           (uint32_t)(y & 7) * 2u;
 }
 
-// v = x0 + x1 + x2 (see the top of the file), four at a time, into the three parts of a tile at `at`.
-__device__ __forceinline__ void muon_split4(const float (&v)[4], uint32_t at, uint32_t plane) {
-    __half h[3][4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float x0 = rintf(v[k]), r = v[k] - x0;
-        h[0][k] = __float2half_rn(x0);
-        h[1][k] = __float2half_rn(r);
-        h[2][k] = __float2half_rn(r - __half2float(h[1][k]));
-    }
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        const __half2 a = __halves2half2(h[i][0], h[i][1]), b = __halves2half2(h[i][2], h[i][3]);
-        ptx::st_shared_v2(at + i * plane, *reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    }
+// v = x0 + x1 + x2 (see the top of the file).  |v| <= 256, so adding 1.5 2^23 rounds to an integer.
+__device__ __forceinline__ void muon_split2(float a, float b, uint32_t (&h)[3]) {
+    constexpr float kRound = 12582912.f;
+    const float a0 = __fadd_rn(__fadd_rn(a, kRound), -kRound), b0 = __fadd_rn(__fadd_rn(b, kRound), -kRound);
+    const float ra = a - a0, rb = b - b0;
+    const __half2 h0 = __floats2half2_rn(a0, b0), h1 = __floats2half2_rn(ra, rb);
+    const float2 f1 = __half22float2(h1);
+    const __half2 h2 = __floats2half2_rn(ra - f1.x, rb - f1.y);
+    h[0] = *reinterpret_cast<const uint32_t*>(&h0);
+    h[1] = *reinterpret_cast<const uint32_t*>(&h1);
+    h[2] = *reinterpret_cast<const uint32_t*>(&h2);
 }
-// Byte offset of quad (row, x) in one part of a tile, 128-byte swizzled: rows of 64 elements; in a tall
-// matrix's tile, 64-row groups of m (x / 16) of 64 columns each.
-__device__ __forceinline__ uint32_t muon_quad_at(bool tall, int row, int x) {
-    const uint32_t group = tall ? (uint32_t)(x >> 4) * 8192u : 0u, y = (uint32_t)x & 15u;
-    return group + (uint32_t)row * 128u + (((y >> 1) ^ ((uint32_t)row & 7u)) << 4) + (y & 1u) * 8u;
-}
+
+// How T threads hold a step of TL columns of a tile of ROWS rows, 16 elements each, in the order of memory:
+//   kRows    not tall, L % 4 == 0: quads of 4 columns of a row
+//   kFlat    tall, w = J s a multiple of 4: quads of the step's TL w consecutive elements
+//   kPairs   tall, other w: pairs of consecutive rows m of a column l'
+//   kQuads   what is left (a tall pair of 64-row groups of s > 128, an odd L): quads, each checked
+// col0: the step's first column in its tile.
+template <int T, int TL, int ROWS>
+struct MuonTile {
+    enum { kRows, kFlat, kPairs, kQuads };
+    static constexpr int NQ = ROWS * TL / 4 / T;
+    static_assert(NQ == 4, "16 elements per thread");
+    static constexpr int kPairCols = T / (ROWS / 2);   // columns l' that the threads' pairs cover at once
+    static constexpr int kRowStep = T / (TL / 4);      // rows that the threads' quads cover at once (not tall)
+    static constexpr int kColStep = T / (ROWS / 4);    // columns that the threads' quads cover at once (tall)
+    static_assert(kRowStep % 8 == 0, "the swizzle repeats every eight rows");
+    int mode, row, x, lo64, hi64;
+    int meta[NQ];      // kRows: the quad's first element in tile 0; kFlat: its place in the tile; -1: none
+
+    // whole: the tile's rows are the whole short side (J stacked blocks of it); otherwise rows 0 and 64 are the
+    // short-side indices lo and hi.
+    __device__ __forceinline__ void enter(const MuonMat& M, int tid, bool whole, int lo, int hi) {
+        const int w = M.J * M.s;
+        lo64 = lo;
+        hi64 = hi;
+        mode = M.tall ? (!whole ? kQuads : (w & 3) ? kPairs : kFlat) : (M.L & 3) ? kQuads : kRows;
+        const int per = mode == kPairs ? ROWS / 2 : M.tall ? ROWS / 4 : TL / 4;
+        row = mode == kFlat ? tid : tid / per;
+        x = mode == kFlat ? 0 : (tid - row * per) * (mode == kPairs ? 2 : 4);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            meta[i] = -1;
+            if (mode == kFlat) {
+                const int f = 4 * (tid + i * T), l = f / w, m = f - l * w;
+                if (l < TL) meta[i] = (int)muon_elem_at(l, m);
+            } else if (mode == kRows) {
+                const int r = row + i * kRowStep;
+                int j = 0, c = r;
+                if (M.J > 1) { j = r / M.s; c = r - j * M.s; }
+                else if (ROWS == 128) c = r + (r < 64 ? lo64 : hi64 - 64);
+                if (j < M.J && c < M.s) meta[i] = c * M.L + j * kMuonTileL + x;
+            }
+        }
+    }
+    // Quad i where each is checked: its first element, and how many exist.
+    __device__ __forceinline__ int quad(const MuonMat& M, int tile, int col0, int i, int& n) const {
+        if (!M.tall) {
+            const int r = row + i * kRowStep;
+            int j = 0, c = r;
+            if (M.J > 1) { j = r / M.s; c = r - j * M.s; }
+            else if (ROWS == 128) c = r + (r < 64 ? lo64 : hi64 - 64);
+            const int l = (tile * M.J + j) * kMuonTileL + col0 + x;
+            n = j < M.J && c < M.s ? max(0, min(4, M.L - l)) : 0;
+            return c * M.L + l;
+        }
+        const int l = tile * kMuonTileL + col0 + row + i * kColStep;      // (a tall pair of groups: J = 1)
+        const int c = x + (x < 64 ? lo64 : hi64 - 64);
+        n = l < M.L ? max(0, min(4, M.s - c)) : 0;
+        return l * M.s + c;
+    }
+    static __device__ __forceinline__ void set4(float (&v)[4], float4 f) { v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w; }
+    static __device__ __forceinline__ float4 get4(const float* p, int e, bool ok) {
+        return ok ? *reinterpret_cast<const float4*>(p + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+
+    // g and m of a step (zeros for what does not exist)
+    __device__ __forceinline__ void load(const MuonMat& M, int tile, int col0, float (&g)[NQ][4], float (&m)[NQ][4]) const {
+        const float *pg = M.g, *pm = M.m;
+        if (mode == kRows && tile + 1 < M.tiles) {
+            const int t0 = tile * kMuonTileL * M.J + col0;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                set4(g[i], get4(pg, meta[i] + t0, meta[i] >= 0));
+                set4(m[i], get4(pm, meta[i] + t0, meta[i] >= 0));
+            }
+        } else if (mode == kFlat) {
+            const int e0 = (tile * kMuonTileL + col0) * M.J * M.s + 4 * row, total = M.L * M.s;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                const bool ok = meta[i] >= 0 && e0 + 4 * T * i < total;
+                set4(g[i], get4(pg, e0 + 4 * T * i, ok));
+                set4(m[i], get4(pm, e0 + 4 * T * i, ok));
+            }
+        } else if (mode == kPairs) {
+            const int w = M.J * M.s, total = M.L * M.s, e0 = (tile * kMuonTileL + col0 + row) * w + x;
+#pragma unroll
+            for (int p = 0; p < 2 * NQ; ++p) {
+                const int e = e0 + p * kPairCols * w;
+                const bool a = x < w && e < total, b = x + 1 < w && e + 1 < total;
+                g[p >> 1][(p & 1) * 2] = a ? pg[e] : 0.f;
+                g[p >> 1][(p & 1) * 2 + 1] = b ? pg[e + 1] : 0.f;
+                m[p >> 1][(p & 1) * 2] = a ? pm[e] : 0.f;
+                m[p >> 1][(p & 1) * 2 + 1] = b ? pm[e + 1] : 0.f;
+            }
+        } else {
+            const bool vec = ((M.tall ? M.s : M.L) & 3) == 0;      // whole quads or none
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                int n;
+                const int e = quad(M, tile, col0, i, n);
+                if (vec) {
+                    set4(g[i], get4(pg, e, n > 0));
+                    set4(m[i], get4(pm, e, n > 0));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        g[i][k] = k < n ? pg[e + k] : 0.f;
+                        m[i][k] = k < n ? pm[e + k] : 0.f;
+                    }
+                }
+            }
+        }
+    }
+    // The same into this thread's own 16-byte cells at `raw` (g's NQ, then m's, T cells apart), asynchronously.
+    __device__ __forceinline__ void fetch(const MuonMat& M, int tile, int col0, uint8_t* raw) const {
+        const float *pg = M.g, *pm = M.m;
+        uint8_t* const rm = raw + NQ * T * 16;
+        auto quads = [&](int i, int e, bool ok) {
+            ptx::cp_async16(raw + i * T * 16, ok ? pg + e : pg, ok ? 16 : 0);
+            ptx::cp_async16(rm + i * T * 16, ok ? pm + e : pm, ok ? 16 : 0);
+        };
+        auto single = [&](int i, int k, int e, bool ok) {
+            ptx::cp_async4(ptx::smem_u32(raw) + i * T * 16 + k * 4, ok ? pg + e : pg, ok ? 4 : 0);
+            ptx::cp_async4(ptx::smem_u32(rm) + i * T * 16 + k * 4, ok ? pm + e : pm, ok ? 4 : 0);
+        };
+        if (mode == kRows && tile + 1 < M.tiles) {
+            const int t0 = tile * kMuonTileL * M.J + col0;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) quads(i, meta[i] + t0, meta[i] >= 0);
+        } else if (mode == kFlat) {
+            const int e0 = (tile * kMuonTileL + col0) * M.J * M.s + 4 * row, total = M.L * M.s;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) quads(i, e0 + 4 * T * i, meta[i] >= 0 && e0 + 4 * T * i < total);
+        } else if (mode == kPairs) {
+            const int w = M.J * M.s, total = M.L * M.s, e0 = (tile * kMuonTileL + col0 + row) * w + x;
+#pragma unroll
+            for (int p = 0; p < 2 * NQ; ++p) {
+                const int e = e0 + p * kPairCols * w;
+                single(p >> 1, (p & 1) * 2, e, x < w && e < total);
+                single(p >> 1, (p & 1) * 2 + 1, e + 1, x + 1 < w && e + 1 < total);
+            }
+        } else {
+            const bool vec = ((M.tall ? M.s : M.L) & 3) == 0;      // whole quads or none
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                int n;
+                const int e = quad(M, tile, col0, i, n);
+                if (vec) {
+                    quads(i, e, n > 0);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) single(i, k, e + k, k < n);
+                }
+            }
+        }
+    }
+    static __device__ __forceinline__ void read(const uint8_t* raw, float (&g)[NQ][4], float (&m)[NQ][4]) {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            set4(g[i], *reinterpret_cast<const float4*>(raw + i * T * 16));
+            set4(m[i], *reinterpret_cast<const float4*>(raw + (NQ + i) * T * 16));
+        }
+    }
+    // stores v to where load() took it from in `dst`
+    __device__ __forceinline__ void store(const MuonMat& M, float* dst, int tile, int col0, const float (&v)[NQ][4]) const {
+        if (mode == kRows && tile + 1 < M.tiles) {
+            const int t0 = tile * kMuonTileL * M.J + col0;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i)
+                if (meta[i] >= 0)
+                    *reinterpret_cast<float4*>(dst + meta[i] + t0) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+        } else if (mode == kFlat) {
+            const int e0 = (tile * kMuonTileL + col0) * M.J * M.s + 4 * row, total = M.L * M.s;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i)
+                if (meta[i] >= 0 && e0 + 4 * T * i < total)
+                    *reinterpret_cast<float4*>(dst + e0 + 4 * T * i) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+        } else if (mode == kPairs) {
+            const int w = M.J * M.s, total = M.L * M.s, e0 = (tile * kMuonTileL + col0 + row) * w + x;
+#pragma unroll
+            for (int p = 0; p < 2 * NQ; ++p) {
+                const int e = e0 + p * kPairCols * w;
+                if (x < w && e < total) dst[e] = v[p >> 1][(p & 1) * 2];
+                if (x + 1 < w && e + 1 < total) dst[e + 1] = v[p >> 1][(p & 1) * 2 + 1];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                int n;
+                const int e = quad(M, tile, col0, i, n);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < n) dst[e + k] = v[i][k];
+            }
+        }
+    }
+    // The three parts of scale * v into the tile at `base`.  Elements of the tile past the matrix's end are
+    // zeros; rows past the matrix's are left alone.
+    __device__ __forceinline__ void put(const MuonMat& M, uint32_t base, uint32_t plane, int col0, float scale,
+                                        const float (&v)[NQ][4]) const {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            uint32_t a[3], b[3];
+            muon_split2(v[i][0] * scale, v[i][1] * scale, a);
+            muon_split2(v[i][2] * scale, v[i][3] * scale, b);
+            if (mode == kPairs) {
+                if (x < M.J * M.s) {
+                    const uint32_t aa = base + muon_elem_at(col0 + row + 2 * i * kPairCols, x);
+                    const uint32_t bb = base + muon_elem_at(col0 + row + (2 * i + 1) * kPairCols, x);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) {
+                        ptx::st_shared_u32(aa + p * plane, a[p]);
+                        ptx::st_shared_u32(bb + p * plane, b[p]);
+                    }
+                }
+                continue;
+            }
+            uint32_t at;
+            bool ok = true;
+            if (mode == kFlat) { at = base + (uint32_t)(meta[i] + col0 * 128); ok = meta[i] >= 0; }
+            else if (mode == kRows) { at = base + muon_elem_at(row, col0 + x) + (uint32_t)(i * kRowStep) * 128u; ok = meta[i] >= 0; }
+            else if (!M.tall) at = base + muon_elem_at(row + i * kRowStep, col0 + x);
+            else at = base + muon_elem_at(col0 + row + i * kColStep, x);
+            if (ok) {
+#pragma unroll
+                for (int p = 0; p < 3; ++p) ptx::st_shared_v2(at + p * plane, a[p], b[p]);
+            }
+        }
+    }
+};
 
 // D0 += a0 b0, D1 += the products of a lower order, over one K step; the parts of an operand lie
 // `astep` / `bstep` (in descriptor units of 16 bytes) apart.
@@ -177,27 +355,58 @@ __device__ __forceinline__ void muon_mma(uint32_t d0, uint32_t d1, uint64_t a, u
 }
 
 // ---------------------------------------------------------------------------------------------- Gram
-constexpr int kGramThreads = 256;
-constexpr int kGramStage = 3 * kMuonPlane;
-constexpr int kGramSmem = 2 * kGramStage + 1024;
+// x 2^k as a double, from the bits of a finite x (a conversion instruction is several times slower than
+// these four); what is below the smallest normal float becomes 0.
+__device__ __forceinline__ double muon_to_double(float x, int k) {
+    const uint32_t b = __float_as_uint(x), mag = b & 0x7fffffffu;
+    const uint32_t hi = (b & 0x80000000u) | ((mag >> 3) + ((uint32_t)(1023 - 127 + k) << 20));
+    return mag < 0x00800000u ? 0.0 : __hiloint2double((int)hi, (int)(b << 29));
+}
 
-// One item: the partial Gram matrix of up to 16 tiles over one pair of 64-row groups (the only pair for
-// s <= 128).  The next tile's g and m are requested before this one is split, and its products run while
-// the next tile is loaded and split (two stages); two blocks per SM.
-// The scale of the split is a power of two above the first tile's largest |u|.  A tile that exceeds it
-// takes the sums out of the accumulators and starts them anew at its own scale.
-__global__ void __launch_bounds__(kGramThreads, 2)
+constexpr int kGramLoad = 512;          // threads that load and split, warps 0 .. 15
+constexpr int kGramThreads = kGramLoad + 32;   // and a warp that issues the products
+constexpr int kGramStage = 3 * kMuonPlane;
+constexpr int kGramRaw = 128 * kMuonTileL * 8; // a tile's g and m
+constexpr int kGramSmem = 2 * kGramStage + 2 * kGramRaw + 1024;
+static_assert(kGramSmem + 1024 <= 232448, "shared memory per CTA");
+constexpr int kGramExactTiles = 16;     // tiles whose x0 x0 sums stay below 2^24 (|x0| <= 128, 64 columns each)
+
+// One item: the partial Gram matrix (of its two equal halves the elements [c][r], c <= r) of a run of tiles
+// over one pair of 64-row groups (the only pair for s <= 128).  Sixteen warps copy a tile's g and m to shared memory (two tiles ahead, every thread
+// its own elements) and split u into one of two places; a further warp issues a place's products.
+// The scale of the split is a power of two, 1.5 to 3 times the first tile's largest |u|.  A tile that exceeds it
+// takes the sums out of the accumulators and starts them anew at its own scale, and so does every 16th tile.
+__global__ void __launch_bounds__(kGramThreads, 1)
 muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_t timeout_ns) {
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) uint64_t done[2];
+    enum { kAdd, kStart, kStop };                 // what the products of a place do to the accumulators
+    __shared__ __align__(8) uint64_t full[2], done[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
-    __shared__ float red[kGramThreads / 32];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    __shared__ volatile int what[2];
+    __shared__ float red[kGramLoad / 32];
     __shared__ MuonMat record;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     muon_fetch(&record, mats + muon_find(0, n - 1, blockIdx.x, [&](int k) { return mats[k].gram0; }));
+    if (tid == 0) {
+        for (int k = 0; k < 2; ++k) {
+            ptx::mbar_init(&full[k], kGramLoad / 32);
+            ptx::mbar_init(&done[k], 1);
+        }
+        abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == kGramLoad / 32) {
+        ptx::tmem_alloc<256>(&tmem_slot);
+        ptx::tmem_relinquish();
+    }
+    // rows past the matrix's stay zero (their products reach no output, but must not be NaN)
+    for (int e = tid; e < 2 * kGramStage / 16; e += kGramThreads) reinterpret_cast<uint4*>(smem)[e] = make_uint4(0, 0, 0, 0);
+    ptx::fence_proxy_async_smem();
+    ptx::tc_fence_before();
     __syncthreads();
+    ptx::tc_fence_after();
     const MuonMat& M = record;
     const int item = blockIdx.x - M.gram0;
     const int chunk = item / M.npairs;
@@ -205,191 +414,207 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
     const int ng = (M.s + 63) / 64;
     for (int k = item - chunk * M.npairs; k > 0; --k)
         if (++gb >= ng) { ++ga; gb = ga + 1; }
-    const int t0 = chunk * kMuonGramTiles, t1 = min(M.tiles, t0 + kMuonGramTiles);
-    const bool vec = muon_aligned(M);
-
-    if (tid == 0) {
-        ptx::mbar_init(&done[0], 1);
-        ptx::mbar_init(&done[1], 1);
-        abort_flag = 0;
-        ptx::fence_barrier_init();
-    }
-    if (warp == 0) {
-        ptx::tmem_alloc<256>(&tmem_slot);
-        ptx::tmem_relinquish();
-    }
-    // rows past the matrix's stay zero (their products reach no output, but must not be NaN)
-    for (int e = tid; e < 2 * kGramStage / 16; e += kGramThreads) reinterpret_cast<uint4*>(smem)[e] = make_uint4(0, 0, 0, 0);
-    ptx::tc_fence_before();
-    __syncthreads();
-    ptx::tc_fence_after();
+    const int t0 = chunk * M.per_chunk, t1 = min(M.tiles, t0 + M.per_chunk);
     const uint32_t tmem = tmem_slot;
     const uint32_t s0 = ptx::smem_u32(smem);
-    const uint32_t idesc = ptx::idesc_f16_f32(128, 128, M.tall != 0, M.tall != 0);
-    // this thread's quads: row + i * rstep, x
-    const int row = M.tall ? tid >> 5 : tid >> 4, x = M.tall ? tid & 31 : tid & 15, rstep = M.tall ? 8 : 16;
 
-    float g[8][4], m[8][4];
-    auto load = [&](int tile) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const MuonQuad q = muon_quad(M, tile, row + i * rstep, x, ga * 64, gb * 64);
-            muon_load4(M.g, q, vec, g[i]);
-            muon_load4(M.m, q, vec, m[i]);
-        }
-    };
-    uint32_t used = 0;      // uses of each stage so far (bits 0, 1: parity of its next completion)
-    int pending = -1;       // stage of the last products issued
-    auto wait_stage = [&](int st) {
-        ptx::mbar_wait(&done[st], ((used >> st) & 1u) ^ 1u, &abort_flag, timeout_ns, err_flag);
-        ptx::tc_fence_after();
-    };
-    float scale = 0.f, unscale = 0.f;
-    bool stored = false;
-    float item_max = 0.f;
-    bool bad = false;
+    if (warp < kGramLoad / 32) {
+        using Tile = MuonTile<kGramLoad, kMuonTileL, 128>;
+        Tile T;
+        T.enter(M, tid, M.npairs == 1, ga * 64, gb * 64);
+        uint8_t* const raw_cells = smem + 2 * kGramStage + tid * 16;
+        T.fetch(M, t0, 0, raw_cells);
+        ptx::cp_async_commit();
+        if (t0 + 1 < t1) T.fetch(M, t0 + 1, 0, raw_cells + kGramRaw);
+        ptx::cp_async_commit();
+        const float mu = M.mu;
+        const bool nesterov = M.nesterov != 0;
+        uint32_t count = 0;     // tiles handed over: the k-th went to place k & 1
+        int since = 0;          // tiles in the accumulators
+        float scale = 0.f;      // 2^-unit
+        int unit = 0;
+        bool stored = false, bad = false;
+        float item_max = 0.f;
+        // the products of the k-th tile have ended
+        auto wait_step = [&](uint32_t k) {
+            ptx::mbar_wait_many(&done[k & 1], (k >> 1) & 1u, &abort_flag, timeout_ns, err_flag);
+            ptx::tc_fence_after();
+        };
+        auto sync = [&] { ptx::named_bar_sync(1, kGramLoad); };
 
-    // Adds the accumulators, in units of unscale^2, to the item's partial.
-    auto drain = [&]() {
-        wait_stage(pending);
-        double* out = M.part + (int64_t)chunk * M.s * M.s;
-        const double us = (double)unscale * (double)unscale;
-        const int r = (warp & 3) * 32 + lane, half = warp >> 2;
-        const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        double* stack = reinterpret_cast<double*>(smem);   // [128][s], the diagonal blocks' rows
-        if (M.J > 1) __syncthreads();                      // every warp has seen the products complete
-        for (int c0 = half * 64; c0 < half * 64 + 64; c0 += 16) {
-            uint32_t hi[16], lo[16];
-            ptx::tmem_ld16(t_row + c0, hi);
-            ptx::tmem_ld16(t_row + 128 + c0, lo);
-            ptx::tmem_ld_wait();
+        // Adds the accumulators, in units of 2^(2 unit), to the item's partial.
+        auto drain = [&]() {
+            wait_step(count - 1);
+            double* out = M.part + (int64_t)chunk * M.s * M.s;
+            const int k2 = 2 * unit;
+            const int r = (warp & 3) * 32 + lane, part = warp >> 2;
+            const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+            double* stack = reinterpret_cast<double*>(smem);   // [s][128], the diagonal blocks' columns
+            const int j = M.J > 1 ? r / M.s : 0;
+            if (M.J > 1) sync();                               // every warp has seen the products end
+            for (int c0 = part * 16; c0 < 128; c0 += 64) {     // the four warps of these rows take turns
+                // only columns up to the warp's last row are needed
+                if (c0 > (warp & 3) * 32 + 31) break;
+                uint32_t hi[16], lo[16];
+                ptx::tmem_ld16(t_row + c0, hi);
+                ptx::tmem_ld16(t_row + 128 + c0, lo);
+                ptx::tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const int c = c0 + k;
-                const double v = ((double)__uint_as_float(hi[k]) + (double)__uint_as_float(lo[k])) * us;
-                if (M.J > 1) {
-                    const int j = r / M.s;
-                    if (j < M.J && c >= j * M.s && c < (j + 1) * M.s) stack[(int64_t)r * M.s + (c - j * M.s)] = v;
-                } else {
-                    const int gr = r < 64 ? ga : gb, gc = c < 64 ? ga : gb;
-                    const int rr = gr * 64 + (r & 63), cc = gc * 64 + (c & 63);
-                    // a diagonal block is in several pairs: the pair with the next group writes it (the last
-                    // group's, the pair with the one before)
-                    const bool own = gr != gc || (gr == ga ? gb == ga + 1 : ga == ng - 2) || ng == 1;
-                    if (own && rr < M.s && cc < M.s) {
-                        double* o = out + (int64_t)rr * M.s + cc;
-                        *o = stored ? *o + v : v;
+                for (int k = 0; k < 16; ++k) {
+                    const int c = c0 + k;
+                    if (c > r) continue;
+                    const double v = muon_to_double(__uint_as_float(hi[k]), k2) + muon_to_double(__uint_as_float(lo[k]), k2);
+                    if (M.J > 1) {
+                        if (j < M.J && c >= j * M.s) stack[(c - j * M.s) * 128 + r] = v;
+                    } else {
+                        const int gr = r < 64 ? ga : gb, gc = c < 64 ? ga : gb;
+                        const int rr = gr * 64 + (r & 63), cc = gc * 64 + (c & 63);
+                        // a diagonal block is in several pairs: the pair with the next group writes it (the last
+                        // group's, the pair with the one before)
+                        const bool own = gr != gc || (gr == ga ? gb == ga + 1 : ga == ng - 2);
+                        if (own && rr < M.s && cc < M.s) {
+                            double* o = out + cc * M.s + rr;      // lanes on consecutive addresses
+                            *o = stored ? *o + v : v;
+                        }
                     }
                 }
             }
-        }
-        if (M.J > 1) {
-            __syncthreads();
-            for (int e = tid; e < M.s * M.s; e += kGramThreads) {
-                double v = 0.0;
-                for (int j = 0; j < M.J; ++j) v += stack[(int64_t)j * M.s * M.s + e];
-                out[e] = stored ? out[e] + v : v;
+            if (M.J > 1) {
+                sync();
+                const int s2 = M.s * M.s;
+                for (int e = tid; e < s2; e += kGramLoad) {
+                    const int cc = e / M.s, rr = e - cc * M.s;
+                    if (cc > rr) continue;
+                    double v = 0.0;
+                    for (int q = 0; q < M.J; ++q) v += stack[cc * 128 + q * M.s + rr];
+                    out[e] = stored ? out[e] + v : v;
+                }
+                sync();
+                // the stages held sums: clear their rows again
+                for (int e = tid; e < 2 * kGramStage / 16; e += kGramLoad)
+                    reinterpret_cast<uint4*>(smem)[e] = make_uint4(0, 0, 0, 0);
             }
-            __syncthreads();
-            // the stages held sums: clear their rows again
-            for (int e = tid; e < 2 * kGramStage / 16; e += kGramThreads)
-                reinterpret_cast<uint4*>(smem)[e] = make_uint4(0, 0, 0, 0);
-            __syncthreads();
-        }
-        ptx::tc_fence_before();
-        stored = true;
-        pending = -1;
-    };
+            ptx::tc_fence_before();
+            sync();
+            stored = true;
+            since = 0;
+        };
+        // hands a place to the issuing warp
+        auto hand_over = [&](int todo) {
+            if (tid == 0) what[count & 1] = todo;
+            ptx::fence_proxy_async_smem();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&full[count & 1]);
+            ++count;
+        };
 
-    load(t0);
-    for (int t = t0; t < t1; ++t) {
-        float u[8][4];
-        float big = 0.f;
-        bool over = false;
+        for (int t = t0; t < t1; ++t) {
+            float u[Tile::NQ][4];
+            {
+                float g[Tile::NQ][4], m[Tile::NQ][4];
+                uint8_t* const cells = raw_cells + ((t - t0) & 1) * kGramRaw;
+                ptx::cp_async_wait<1>();
+                Tile::read(cells, g, m);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < Tile::NQ; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                u[i][k] = muon_u(M, muon_m(M, m[i][k], g[i][k]), g[i][k]);
-                const float a = fabsf(u[i][k]);
-                over = over || !(a * scale <= 128.f);      // also a NaN
-                big = fmaxf(big, a);
+                    for (int k = 0; k < 4; ++k) {
+                        const float mn = fmaf(mu, m[i][k], g[i][k]);
+                        u[i][k] = nesterov ? fmaf(mu, mn, g[i][k]) : mn;
+                    }
+                if (t + 2 < t1) T.fetch(M, t + 2, 0, cells);
+                ptx::cp_async_commit();
             }
-        if (t + 1 < t1) load(t + 1);
-        item_max = fmaxf(item_max, big);
-        // the first tile has no scale yet; a first tile of zeros leaves it to the next
-        if (__syncthreads_or(over || scale == 0.f)) {
-            if (pending >= 0) drain();
-            float w = big;
-            bool nan = over && !(big * 0.f == 0.f);
+            float big = 0.f;
+            bool over = scale == 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < Tile::NQ; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) nan = nan || !(u[i][k] * 0.f == 0.f);
-            for (int o = 16; o > 0; o >>= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, o));
-            if (lane == 0) red[warp] = w;
-            bad = __syncthreads_or(nan) || bad;
-            w = 0.f;
-            for (int k = 0; k < kGramThreads / 32; ++k) w = fmaxf(w, red[k]);
-            if (!bad && w > 0.f) {
-                const int e = max(ilogbf(w) + 1, -100);    // w < 2^e
-                scale = scalbnf(1.f, 7 - e);
-                unscale = scalbnf(1.f, e - 7);
+                for (int k = 0; k < 4; ++k) {
+                    const float a = fabsf(u[i][k]);
+                    over = over || !(a * scale <= 128.f);      // also a NaN
+                    big = fmaxf(big, a);
+                }
+            item_max = fmaxf(item_max, big);
+            // (the first tile has no scale yet; a first tile of zeros leaves it to the next)
+            over = ptx::named_bar_or(1, kGramLoad, over);
+            if (over || since == kGramExactTiles) {
+                if (since > 0) drain();
+                if (over) {
+                    float w = big;
+                    bool nan = false;
+#pragma unroll
+                    for (int i = 0; i < Tile::NQ; ++i)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) nan = nan || !(u[i][k] * 0.f == 0.f);
+                    for (int o = 16; o > 0; o >>= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, o));
+                    if (lane == 0) red[warp] = w;
+                    bad = ptx::named_bar_or(1, kGramLoad, nan) || bad;
+                    w = 0.f;
+                    for (int k = 0; k < kGramLoad / 32; ++k) w = fmaxf(w, red[k]);
+                    if (!bad && w > 0.f) {
+                        // a power of two at least 1.5 times the largest, so that the next steps' seldom exceed it
+                        unit = max(ilogbf(1.5f * w) + 1, -100) - 7;
+                        scale = scalbnf(1.f, -unit);
+                    }
+                    sync();
+                }
             }
-            __syncthreads();
+            if (bad) break;                     // a NaN or an infinity: the whole matrix becomes NaN
+            if (scale == 0.f) continue;         // nothing but zeros so far
+            if (count >= 2) wait_step(count - 2);              // the products that last read this place
+            T.put(M, s0 + (count & 1) * kGramStage, kMuonPlane, 0, scale, u);
+            hand_over(since == 0 ? kStart : kAdd);
+            ++since;
         }
-        if (bad) break;                     // a NaN or an infinity: the whole matrix becomes NaN
-        if (scale == 0.f) continue;         // nothing but zeros so far
-        const int st = t & 1;
-        const uint32_t base = s0 + st * kGramStage;
-        if ((used >> (2 + st)) & 1u) wait_stage(st);       // the products that last read this stage
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = u[i][k] * scale;
-            muon_split4(v, base + muon_quad_at(M.tall, row + i * rstep, x), kMuonPlane);
+        if (since > 0) drain();
+        if (count >= 2) wait_step(count - 2);
+        hand_over(kStop);
+        // nothing but zeros, or a NaN or an infinity somewhere in the item
+        if (!stored || bad) {
+            sync();
+            double* out = M.part + (int64_t)chunk * M.s * M.s;
+            const double v = bad ? __longlong_as_double(0x7ff8000000000000ll) : 0.0;
+            for (int e = tid; e < M.s * M.s; e += kGramLoad) {
+                const int r = e / M.s, c = e - r * M.s, gr = r >> 6, gc = c >> 6;
+                if (M.npairs == 1 || ((gr == ga || gr == gb) && (gc == ga || gc == gb) &&
+                                      (gr != gc || (gr == ga ? gb == ga + 1 : ga == ng - 2))))
+                    out[e] = v;
+            }
         }
-        ptx::fence_proxy_async_smem();
-        ptx::tc_fence_before();
-        __syncthreads();
-        ptx::tc_fence_after();
+        for (int o = 16; o > 0; o >>= 1) item_max = fmaxf(item_max, __shfl_xor_sync(0xffffffffu, item_max, o));
+        if (lane == 0) red[warp] = item_max;
+        sync();
         if (tid == 0) {
-            const uint64_t d = M.tall ? ptx::smem_desc_sw128(base, 8192, 1024) : ptx::smem_desc_sw128(base, 16, 1024);
-            const uint64_t kstep = M.tall ? 2048 / 16 : 32 / 16;
-            for (int ks = 0; ks < kMuonTileL / 16; ++ks)
-                muon_mma(tmem, tmem + 128, d + ks * kstep, d + ks * kstep, kMuonPlane / 16, kMuonPlane / 16, idesc,
-                         pending < 0 && ks == 0);
-            ptx::tc_commit(&done[st]);
+            float w = 0.f;
+            for (int k = 0; k < kGramLoad / 32; ++k) w = fmaxf(w, red[k]);
+            M.hdr[2 + item] = w;
         }
-        used ^= 1u << st;
-        used |= 4u << st;
-        pending = st;
-    }
-    if (pending >= 0) drain();
-    // nothing but zeros, or a NaN or an infinity somewhere in the item
-    if (!stored || bad) {
-        __syncthreads();
-        double* out = M.part + (int64_t)chunk * M.s * M.s;
-        const double v = bad ? __longlong_as_double(0x7ff8000000000000ll) : 0.0;
-        for (int e = tid; e < M.s * M.s; e += kGramThreads) {
-            const int r = e / M.s, c = e - r * M.s, gr = r >> 6, gc = c >> 6;
-            if (M.npairs == 1 || ((gr == ga || gr == gb) && (gc == ga || gc == gb) &&
-                                  (gr != gc || (gr == ga ? gb == ga + 1 : ga == ng - 2))))
-                out[e] = v;
+    } else if (lane == 0) {
+        const bool tall = M.tall != 0;
+        const uint32_t idesc = ptx::idesc_f16_f32(128, 128, tall, tall);
+        for (uint32_t k = 0;; ++k) {
+            const int place = k & 1;
+            if (!ptx::mbar_wait_many(&full[place], (k >> 1) & 1u, &abort_flag, timeout_ns, err_flag)) break;
+            const int todo = what[place];
+            if (todo == kStop) break;
+            ptx::tc_fence_after();
+            const uint32_t base = s0 + place * kGramStage;
+            const uint64_t kstep = tall ? 2048 / 16 : 32 / 16;
+            const uint64_t d = tall ? ptx::smem_desc_sw128(base, 8192, 1024) : ptx::smem_desc_sw128(base, 16, 1024);
+#pragma unroll
+            for (int q = 0; q < kMuonTileL / 16; ++q)
+                muon_mma(tmem, tmem + 128, d + q * kstep, d + q * kstep, kMuonPlane / 16, kMuonPlane / 16, idesc,
+                         todo == kStart && q == 0);
+            ptx::tc_commit(&done[place]);
         }
     }
-    for (int o = 16; o > 0; o >>= 1) item_max = fmaxf(item_max, __shfl_xor_sync(0xffffffffu, item_max, o));
-    if (lane == 0) red[warp] = item_max;
+    __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (tid == 0) {
-        float w = 0.f;
-        for (int k = 0; k < kGramThreads / 32; ++k) w = fmaxf(w, red[k]);
-        M.hdr[2 + item] = w;
-    }
-    if (warp == 0) ptx::tmem_dealloc<256>(tmem);
+    if (warp == kGramLoad / 32) ptx::tmem_dealloc<256>(tmem);
 }
 
 // ----------------------------------------------------------------------------------------- iteration
@@ -406,60 +631,89 @@ __device__ __forceinline__ void dmma_16x8x8(double (&d)[4], const double (&a)[4]
         : "d"(a[0]), "d"(a[1]), "d"(a[2]), "d"(a[3]), "d"(b[0]), "d"(b[1]));
 }
 
-// C = A B for symmetric sp x sp matrices that commute (so C is symmetric and B's rows serve as its
-// columns): the 32 x 32 tiles of C's lower half, dealt over the cluster's blocks, each with its K in
-// stages of 64 that run ahead across tiles.  out(r, c, v) takes each element with c <= r.  Eight warps: 2 x 2
-// blocks of 16 x 16, two halves of each stage's K, joined in a fixed order.
+// One product of the iteration: C = A B for symmetric sp x sp matrices that commute, so that C is symmetric
+// (only elements with c <= r are computed) and B's rows serve as its columns.
+struct NsProduct {
+    const double* A;
+    const double* B;
+    int what;          // passed on to `out`
+};
+
+// Up to two products over a cluster: the 32 x 32 tiles of their lower halves dealt over its blocks, each with
+// its K in stages of 64 that run ahead across tiles.  out(what, r, c, v) takes each element.
+// Eight warps: 2 x 2 blocks of 16 x 16, two interleaved halves of each stage's K, joined in a fixed order.
 template <typename F>
-__device__ __forceinline__ void ns_product(const double* A, const double* B, int sp, int rank, double* sm, F&& out) {
+__device__ __forceinline__ void ns_products(const NsProduct& p0, const NsProduct& p1, int n, int sp, int rank, double* sm,
+                                            F&& out) {
     constexpr int T = kMuonNsTile;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int wr = (warp & 1) * 16, wc = ((warp >> 1) & 1) * 16, kh = warp >> 2;
-    const int nt = (sp + T - 1) / T, tiles = nt * (nt + 1) / 2, nk = (sp + kNsK - 1) / kNsK;
-    const int mine = tiles > rank ? (tiles - rank + kMuonCluster - 1) / kMuonCluster : 0;
-    const int steps = mine * nk;
-    auto tile_of = [&](int k, int& ti, int& tj) {
-        int t = rank + (k / nk) * kMuonCluster;
-        ti = 0;
-        while (t > ti) { t -= ti + 1; ++ti; }
-        tj = t;
+    const int nt = (sp + T - 1) / T, each = nt * (nt + 1) / 2, tiles = n * each, nk = (sp + kNsK - 1) / kNsK;
+    // a cursor over this block's (tile, K stage) steps
+    struct Cursor {
+        int t, ti, tj, kc, st;
+        bool second;
     };
-    auto fetch = [&](int k) {
-        if (k < steps) {
-            int ti, tj;
-            tile_of(k, ti, tj);
-            const int k0 = (k % nk) * kNsK;
-            double* st = sm + (k % kNsStages) * kNsStageD;
+    auto place = [&](Cursor& c) {
+        int t = c.t;
+        c.second = t >= each;
+        if (c.second) t -= each;
+        c.ti = 0;
+        while (t > c.ti) { t -= c.ti + 1; ++c.ti; }
+        c.tj = t;
+        c.kc = 0;
+    };
+    auto next = [&](Cursor& c) {
+        if (++c.st == kNsStages) c.st = 0;
+        if (++c.kc == nk) {
+            c.t += kMuonCluster;
+            place(c);
+        }
+    };
+    Cursor fc{rank, 0, 0, 0, 0, false};
+    place(fc);
+    Cursor cc = fc;
+    // this thread's pieces of a stage: 16 bytes at column fcol of rows frow + 8 i of A's and of B's tile
+    const int frow = tid >> 5, fcol = (tid & 31) * 2;
+    auto fetch = [&]() {
+        if (fc.t < tiles) {
+            const NsProduct& p = fc.second ? p1 : p0;
+            const int k0 = fc.kc * kNsK + fcol, ra = fc.ti * T + frow, rb = fc.tj * T + frow;
+            const bool kin = k0 < sp;
+            const double* a = p.A + (kin ? ra * sp + k0 : 0);
+            const double* b = p.B + (kin ? rb * sp + k0 : 0);
+            double* dst = sm + fc.st * kNsStageD + frow * kNsPitch + fcol;
 #pragma unroll
-            for (int e0 = 0; e0 < 2 * T * kNsK / 2; e0 += 256) {
-                const int e = e0 + tid, half = e >> 10, r = (e >> 5) & 31, c = (e & 31) * 2;
-                const int gr = (half ? tj : ti) * T + r, gc = k0 + c;
-                const bool ok = gr < sp && gc < sp;
-                const double* src = (half ? B : A) + (ok ? (int64_t)gr * sp + gc : 0);
-                ptx::cp_async16(st + (half * T + r) * kNsPitch + c, src, ok ? 16 : 0);
+            for (int i = 0; i < 4; ++i) {
+                const bool ia = kin && ra + 8 * i < sp, ib = kin && rb + 8 * i < sp;
+                ptx::cp_async16(dst + 8 * i * kNsPitch, ia ? a + 8 * i * sp : p.A, ia ? 16 : 0);
+                ptx::cp_async16(dst + (T + 8 * i) * kNsPitch, ib ? b + 8 * i * sp : p.B, ib ? 16 : 0);
             }
+            next(fc);
         }
         ptx::cp_async_commit();
     };
     double acc[2][4] = {};
-    for (int k = 0; k < kNsStages - 1; ++k) fetch(k);
-    for (int k = 0; k < steps; ++k) {
+    for (int k = 0; k < kNsStages - 1; ++k) fetch();
+    while (cc.t < tiles) {
         ptx::cp_async_wait<kNsStages - 2>();
-        __syncthreads();
-        fetch(k + kNsStages - 1);
-        const double* as = sm + (k % kNsStages) * kNsStageD + (wr + (lane >> 2)) * kNsPitch + (lane & 3) + kh * (kNsK / 2);
-        const double* bs = sm + (k % kNsStages) * kNsStageD + (T + wc + (lane >> 2)) * kNsPitch + (lane & 3) + kh * (kNsK / 2);
+        __syncthreads();                      // the stage is there, and every warp has left the one fetched next
+        fetch();
+        const int kn = sp - cc.kc * kNsK;     // a multiple of 8
+        const double* as = sm + cc.st * kNsStageD + (wr + (lane >> 2)) * kNsPitch + (lane & 3);
+        const double* bs = sm + cc.st * kNsStageD + (T + wc + (lane >> 2)) * kNsPitch + (lane & 3);
 #pragma unroll
-        for (int kk = 0; kk < kNsK / 2; kk += 8) {
-            const double a[4] = {as[kk], as[kk + 8 * kNsPitch], as[kk + 4], as[kk + 8 * kNsPitch + 4]};
-            const double b0[2] = {bs[kk], bs[kk + 4]};
-            const double b1[2] = {bs[kk + 8 * kNsPitch], bs[kk + 8 * kNsPitch + 4]};
-            dmma_16x8x8(acc[0], a, b0);
-            dmma_16x8x8(acc[1], a, b1);
+        for (int q = 0; q < kNsK / 16; ++q) {
+            const int kk = q * 16 + kh * 8;
+            if (kk < kn) {
+                const double a[4] = {as[kk], as[kk + 8 * kNsPitch], as[kk + 4], as[kk + 8 * kNsPitch + 4]};
+                const double b0[2] = {bs[kk], bs[kk + 4]};
+                const double b1[2] = {bs[kk + 8 * kNsPitch], bs[kk + 8 * kNsPitch + 4]};
+                dmma_16x8x8(acc[0], a, b0);
+                dmma_16x8x8(acc[1], a, b1);
+            }
         }
-        if (k % nk == nk - 1) {   // the tile is complete
-            int ti, tj;
-            tile_of(k, ti, tj);
+        if (cc.kc == nk - 1) {   // the tile is complete
             double* red = sm + kNsStages * kNsStageD + ((warp & 3) * 32 + lane) * 8;
             if (kh) {
 #pragma unroll
@@ -473,9 +727,9 @@ __device__ __forceinline__ void ns_product(const double* A, const double* B, int
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int r = ti * T + wr + (lane >> 2) + (i >> 1) * 8, c = tj * T + wc + j * 8 + (lane & 3) * 2 + (i & 1);
-                        // (a diagonal tile's upper half would mirror onto its lower one)
-                        if (r < sp && c <= r) out(r, c, acc[j][i] + red[4 * j + i]);
+                        const int r = cc.ti * T + wr + (lane >> 2) + (i >> 1) * 8;
+                        const int c = cc.tj * T + wc + j * 8 + (lane & 3) * 2 + (i & 1);
+                        if (r < sp && c <= r) out(cc.second ? p1.what : p0.what, r, c, acc[j][i] + red[4 * j + i]);
                     }
             }
 #pragma unroll
@@ -483,8 +737,57 @@ __device__ __forceinline__ void ns_product(const double* A, const double* B, int
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[j][i] = 0.0;
         }
+        next(cc);
     }
     ptx::cp_async_wait<0>();
+    __syncthreads();
+}
+
+// The same for s <= 64 on one block with its matrices in shared memory (pitch kNsPitch): the 10 blocks of
+// 16 x 16 of the lower half over the eight warps, their results kept in registers until every warp has
+// read its operands, so that C may be A or B.
+template <typename F>
+__device__ __forceinline__ void ns_product_small(const double* A, const double* B, int sp, F&& out) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int nt = (sp + 15) / 16, tiles = nt * (nt + 1) / 2;
+    double acc[2][2][4] = {};
+    auto tile_of = [](int t, int& ti, int& tj) {
+        ti = 0;
+        while (t > ti) { t -= ti + 1; ++ti; }
+        tj = t;
+    };
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const int t = warp + 8 * w;
+        if (t >= tiles) continue;
+        int ti, tj;
+        tile_of(t, ti, tj);
+        const double* as = A + (ti * 16 + (lane >> 2)) * kNsPitch + (lane & 3);
+        const double* bs = B + (tj * 16 + (lane >> 2)) * kNsPitch + (lane & 3);
+#pragma unroll 2
+        for (int kk = 0; kk < sp; kk += 8) {
+            const double a[4] = {as[kk], as[kk + 8 * kNsPitch], as[kk + 4], as[kk + 8 * kNsPitch + 4]};
+            const double b0[2] = {bs[kk], bs[kk + 4]};
+            const double b1[2] = {bs[kk + 8 * kNsPitch], bs[kk + 8 * kNsPitch + 4]};
+            dmma_16x8x8(acc[w][0], a, b0);
+            dmma_16x8x8(acc[w][1], a, b1);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const int t = warp + 8 * w;
+        if (t >= tiles) continue;
+        int ti, tj;
+        tile_of(t, ti, tj);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = ti * 16 + (lane >> 2) + (i >> 1) * 8, c = tj * 16 + j * 8 + (lane & 3) * 2 + (i & 1);
+                if (r < sp && c <= r) out(r, c, acc[w][j][i]);
+            }
+    }
     __syncthreads();
 }
 
@@ -496,27 +799,37 @@ __host__ __device__ __forceinline__ int64_t muon_q_at(int kblocks, int row, int 
     return block * kMuonPlane + r * 128 + (((k8 & 7) ^ (r & 7)) << 4);
 }
 
-// The iteration on one matrix's Gram matrix in fp64 on the fp64 tensor cores: a cluster of eight blocks
-// per matrix, the matrices in L2, one cluster barrier after each product.  Then Q's three fp16 parts for
-// the apply pass (block-diagonal over the stacked blocks) and the scales.
+constexpr int kNsSmallS = 64;
+static_assert(3 * kNsSmallS * kNsPitch * 8 <= kMuonNsSmem, "G, P and Q of a small matrix in shared memory");
+
+// The iteration on the matrices' Gram matrices in fp64 on the fp64 tensor cores.  s > 64: a cluster of eight
+// blocks per matrix, the matrices in L2, one cluster barrier after each round of products; s <= 64: one
+// block, the matrices in shared memory.  order: the matrices, those with s > 64 (n_big of them) first.
+// Then Q's three fp16 parts for the apply pass (block-diagonal over the stacked blocks) and the scales.
 __global__ void __cluster_dims__(kMuonCluster, 1, 1) __launch_bounds__(256)
-muon_ns_kernel(const MuonMat* __restrict__ mats) {
+muon_ns_kernel(const MuonMat* __restrict__ mats, const int32_t* __restrict__ order, int n_big, int n) {
     extern __shared__ __align__(16) double sm[];
     __shared__ double redd[8];
     __shared__ float redf[8];
-    const MuonMat M = mats[blockIdx.x / kMuonCluster];
-    const int rank = (int)ptx::cluster_ctarank();
+    __shared__ MuonMat record;
+    const bool small = blockIdx.x >= (unsigned)n_big * kMuonCluster;
+    const int which = small ? n_big + (int)blockIdx.x - n_big * kMuonCluster : (int)blockIdx.x / kMuonCluster;
+    if (which >= n) return;      // the last cluster's spare blocks (their cluster holds small matrices only)
+    muon_fetch(&record, mats + order[which]);
+    __syncthreads();
+    const MuonMat& M = record;
+    const int rank = small ? 0 : (int)ptx::cluster_ctarank(), ranks = small ? 1 : kMuonCluster;
     const int tid = threadIdx.x, s = M.s, sp = (s + 7) & ~7;
-    const int64_t s2 = (int64_t)s * s, n2 = (int64_t)sp * sp;
-    double* G = M.ns;
-    double* P = G + n2;
-    double* R = P + n2;
-    double* Q = R + n2;
+    const int s2 = s * s, pitch = small ? kNsPitch : sp, rows = small ? ((sp + 15) & ~15) : sp;
+    double* G = small ? sm : M.ns;
+    double* P = G + (small ? kNsSmallS * kNsPitch : sp * sp);
+    double* Q = P + (small ? kNsSmallS * kNsPitch : sp * sp);
+    double* R = Q + (small ? 0 : sp * sp);      // (the small products need no fourth matrix)
     // |u|_F^2, the trace of G, and max |u|: by every block in the same order
     double tr = 0.0;
     for (int e = tid; e < s * M.nchunks; e += 256) {
         const int d = e % s, ch = e / s;
-        tr += M.part[ch * s2 + (int64_t)d * (s + 1)];
+        tr += M.part[(int64_t)ch * s2 + d * (s + 1)];
     }
     float big = 0.f;
     for (int e = tid; e < M.nchunks * M.npairs; e += 256) big = fmaxf(big, M.hdr[2 + e]);
@@ -530,79 +843,124 @@ muon_ns_kernel(const MuonMat* __restrict__ mats) {
     big = 0.f;
     for (int w = 0; w < 8; ++w) { tr += redd[w]; big = fmaxf(big, redf[w]); }
     const double inv = 1.0 / (sqrt(tr) + (double)M.eps);
-    for (int64_t e = rank * 256 + tid; e < n2; e += 256 * kMuonCluster) {
-        const int r = (int)(e / sp), c = (int)(e - (int64_t)r * sp);
-        double g = 0.0;
-        if (r < s && c < s)
-            for (int ch = 0; ch < M.nchunks; ++ch) g += M.part[ch * s2 + (int64_t)r * s + c];
-        G[e] = (g * inv) * inv;
+    // G, from the halves of the partials: four elements per thread and four chunks in flight
+    const int step = 256 * ranks, cells = rows * pitch;
+    for (int e0 = rank * 256 + tid; e0 < cells; e0 += 4 * step) {
+        double g[4] = {};
+        int at[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int e = e0 + q * step, r = e / pitch, c = e - r * pitch;
+            at[q] = e < cells && r < s && c < s ? min(r, c) * s + max(r, c) : -1;
+        }
+        int ch = 0;
+        for (; ch + 4 <= M.nchunks; ch += 4) {
+            double v[4][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[k][q] = at[q] >= 0 ? M.part[(int64_t)(ch + k) * s2 + at[q]] : 0.0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) g[q] += v[k][q];
+        }
+        for (; ch < M.nchunks; ++ch)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) g[q] += at[q] >= 0 ? M.part[(int64_t)ch * s2 + at[q]] : 0.0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int e = e0 + q * step;
+            if (e >= cells) continue;
+            G[e] = (g[q] * inv) * inv;
+            if (small) P[e] = Q[e] = 0.0;
+        }
     }
-    auto sync = [] {
-        __threadfence();
-        ptx::cluster_sync();
+    auto sync = [&] {
+        if (small) __syncthreads();
+        else ptx::cluster_sync();
     };
     sync();
     const double a = M.a, b = M.b, c = M.c;
     auto both = [&](double* C, int i, int j, double v) {
-        C[(int64_t)i * sp + j] = v;
-        C[(int64_t)j * sp + i] = v;
+        C[i * pitch + j] = v;
+        C[j * pitch + i] = v;
     };
-    for (int k = 0; k < M.steps; ++k) {
-        const bool last = k + 1 == M.steps;
-        // P = a I + b G + c G^2 (the first step's P is Q_1)
-        ns_product(G, G, sp, rank, sm, [&](int i, int j, double v) {
-            const double p = (i == j && i < s ? a : 0.0) + b * __ldcg(G + (int64_t)i * sp + j) + c * v;
-            both(P, i, j, p);
-            if (k == 0) both(Q, i, j, p);
-        });
-        sync();
-        if (k > 0) {
-            ns_product(P, Q, sp, rank, sm, [&](int i, int j, double v) { both(R, i, j, v); });
-            sync();
-            double* t = Q; Q = R; R = t;
+    if (small) {
+        for (int k = 0; k < M.steps; ++k) {
+            // P = a I + b G + c G^2 (the first step's P is Q_1)
+            ns_product_small(G, G, sp, [&](int i, int j, double v) {
+                const double p = (i == j && i < s ? a : 0.0) + b * G[i * pitch + j] + c * v;
+                both(P, i, j, p);
+                if (k == 0) both(Q, i, j, p);
+            });
+            if (k > 0) ns_product_small(P, Q, sp, [&](int i, int j, double v) { both(Q, i, j, v); });
+            if (k + 1 == M.steps) break;
+            ns_product_small(P, G, sp, [&](int i, int j, double v) { both(G, i, j, v); });
+            ns_product_small(P, G, sp, [&](int i, int j, double v) { both(G, i, j, v); });
         }
-        if (last) break;
-        ns_product(P, G, sp, rank, sm, [&](int i, int j, double v) { both(R, i, j, v); });
-        sync();
-        ns_product(P, R, sp, rank, sm, [&](int i, int j, double v) { both(G, i, j, v); });
-        sync();
+    } else {
+        double* S = R + sp * sp;
+        for (int k = 0; k < M.steps; ++k) {
+            const bool last = k + 1 == M.steps;
+            const NsProduct sq{G, G, 0};
+            ns_products(sq, sq, 1, sp, rank, sm, [&](int, int i, int j, double v) {
+                const double p = (i == j && i < s ? a : 0.0) + b * __ldcg(G + i * sp + j) + c * v;
+                both(P, i, j, p);
+                if (k == 0) both(Q, i, j, p);
+            });
+            sync();
+            // Q <- P Q and R = P G together, then G <- P R
+            const NsProduct two0{P, k ? Q : G, k ? 0 : 1}, two1{P, G, 1};
+            const int n2 = (k ? 1 : 0) + (last ? 0 : 1);
+            if (n2 == 0) break;
+            ns_products(two0, two1, n2, sp, rank, sm, [&](int what, int i, int j, double v) { both(what ? R : S, i, j, v); });
+            sync();
+            if (k) { double* t = Q; Q = S; S = t; }
+            if (last) break;
+            const NsProduct pr{P, R, 0};
+            ns_products(pr, pr, 1, sp, rank, sm, [&](int, int i, int j, double v) { both(G, i, j, v); });
+            sync();
+        }
     }
-    // max |Q|: each block's share, then the eight of them
+    auto q_of = [&](int r, int c) { return small ? Q[r * pitch + c] : __ldcg(Q + r * sp + c); };
+    // max |Q|: each block's share, then all of them
     float* const qpart = M.hdr + 2 + M.nchunks * M.npairs;
     float qmax = 0.f;
-    for (int64_t e = rank * 256 + tid; e < n2; e += 256 * kMuonCluster) qmax = fmaxf(qmax, (float)fabs(__ldcg(Q + e)));
+    for (int e = rank * 256 + tid; e < s2; e += 256 * ranks) qmax = fmaxf(qmax, (float)fabs(q_of(e / s, e % s)));
     for (int o = 16; o > 0; o >>= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, o));
     __syncthreads();
     if ((tid & 31) == 0) redf[tid >> 5] = qmax;
     __syncthreads();
-    if (tid == 0) {
-        for (int w = 1; w < 8; ++w) qmax = fmaxf(qmax, redf[w]);
-        qpart[rank] = qmax;
-    }
-    sync();
     qmax = 0.f;
-    for (int k = 0; k < kMuonCluster; ++k) qmax = fmaxf(qmax, __ldcg(qpart + k));
+    for (int w = 0; w < 8; ++w) qmax = fmaxf(qmax, redf[w]);
+    if (!small) {
+        if (tid == 0) qpart[rank] = qmax;
+        sync();
+        for (int k = 0; k < kMuonCluster; ++k) qmax = fmaxf(qmax, __ldcg(qpart + k));
+    }
     const int eq = qmax > 0.f && qmax < 3e38f ? ilogbf(qmax) + 1 : 0, eu = max(big > 0.f ? ilogbf(big) + 1 : -100, -100);
     const double qs = scalbn(1.0, 8 - eq);
     if (rank == 0 && tid == 0) {
         M.hdr[0] = scalbnf(1.f, 8 - eu);                                      // x = u hdr[0], |x| < 256
         // a NaN or an infinity in u makes the whole of O a NaN
-        const bool fine = tr * 0.0 == 0.0 && qmax < 3e38f && qmax == qmax;
+        const bool fine = tr * 0.0 == 0.0 && qmax < 3e38f;
         M.hdr[1] = fine ? (float)(inv * scalbn(1.0, eu - 8 + eq - 8)) : __int_as_float(0x7fc00000);
     }
     const int w = s > kMuonBigS ? 256 : 128, kblocks = w / 64;
-    for (int e = rank * 256 + tid; e < w * (w / 8); e += 256 * kMuonCluster) {
+    for (int e = rank * 256 + tid; e < w * (w / 8); e += 256 * ranks) {
         const int r = e / (w / 8), k8 = e - r * (w / 8);
         const int jr = r / s, cr = r - jr * s;
+        int jk = k8 * 8 / s, ck = k8 * 8 - jk * s;
         __align__(16) __half h[3][8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const int kk = k8 * 8 + k, jk = kk / s, ck = kk - jk * s;
-            const double v = jr < M.J && jr == jk ? __ldcg(Q + (int64_t)cr * sp + ck) * qs : 0.0;
+            const double v = jr < M.J && jr == jk ? q_of(cr, ck) * qs : 0.0;
             const double x0 = rint(v);
             h[0][k] = __double2half(x0);
             h[1][k] = __double2half(v - x0);
             h[2][k] = __double2half((v - x0) - (double)__half2float(h[1][k]));
+            if (++ck == s) { ck = 0; ++jk; }
         }
 #pragma unroll
         for (int i = 0; i < 3; ++i)
@@ -611,46 +969,56 @@ muon_ns_kernel(const MuonMat* __restrict__ mats) {
 }
 
 // --------------------------------------------------------------------------------------------- apply
-constexpr int kApplyThreads = 512;
-constexpr int kApplyQ = 6 * kMuonPlane;               // Q of s <= 128, or two (half, column block) stages
+constexpr int kApplyLoad = 256;                       // threads that load, split and store m: warps 0 .. 7
+constexpr int kApplyDone = 256;                       // threads that finish p: warps 8 .. 15
+constexpr int kApplyThreads = kApplyLoad + kApplyDone + 128;  // and a warpgroup whose first warp issues the products
+// Registers per thread of the three; the launch has kApplyThreads x 96 (640 threads).
+constexpr int kApplyRegsLoad = 128, kApplyRegsDone = 80, kApplyRegsIssue = 40;
+static_assert(kApplyLoad * kApplyRegsLoad + kApplyDone * kApplyRegsDone + 128 * kApplyRegsIssue <= kApplyThreads * 96,
+              "register shares");
+constexpr int kApplyQ = 6 * kMuonPlane;               // Q of s <= 128, or two (half, column block) pieces
 constexpr int kApplyV = 6 * kMuonPlane;               // two tiles of 128 rows, or one of 256
-constexpr int kApplyWarpStage = 32 * 16 * 4;          // a warp's 32 x 16 block of O
-constexpr int kApplySmem = kApplyQ + kApplyV + (kApplyThreads / 32) * kApplyWarpStage + 1024;
-static_assert(kApplySmem + 128 <= 232448, "shared memory per CTA");
+constexpr int kApplyBlock = 32 * 16 * 4;              // a finishing warp's 32 x 16 block of O
+constexpr int kApplySmem = kApplyQ + kApplyV + (kApplyDone / 32) * kApplyBlock + 1024;
+static_assert(kApplySmem + 1024 <= 232448, "shared memory per CTA");
 
-// O = Q X_0 tile by tile, then p, its bf16 copy and m.  One block per SM over a contiguous run of tiles
-// (all matrices' tiles in one list, so the blocks finish together); Q stays in shared memory while the
-// matrix does.  Per tile: u is formed from the loaded g and m, the new m stored, u split into its parts;
-// the products of this tile run while the previous tile's O is turned into its update and the next
-// tile's g and m arrive.
-// BIG (s > 128): tiles of 256 rows, Q's (half, column block) pieces streamed from L2 through two stages.
+// O = Q X_0 tile by tile, then p, its bf16 copy and m.  One block per SM over a contiguous run of tiles (all
+// matrices' tiles in one list, so that the blocks finish together), with three roles that run side by side:
+//   load     g and m of a step (the next step's are on their way), m <- the new m, u in parts to shared memory
+//   products Q, kept in shared memory while the matrix lasts, times the tile: 64 columns of O in two
+//            accumulators, of two such sets in turn
+//   finish   p (requested before O is there), O out of the accumulators, the new p and its bf16 copy
+// BIG (s > 128): tiles of 256 rows in one place, Q's (row half, column block) pieces streamed from L2.
 template <bool BIG>
 __global__ void __launch_bounds__(kApplyThreads, 1)
 muon_apply_kernel(const MuonMat* __restrict__ mats, int first, int last, int tiles, int* err_flag, uint64_t timeout_ns) {
-    constexpr int NQ = BIG ? 8 : 4;                    // quads per thread
-    constexpr int PLANE = BIG ? 2 * kMuonPlane : kMuonPlane;
-    constexpr int HALVES = BIG ? 2 : 1;
+    constexpr int HALVES = BIG ? 2 : 1, PLACES = BIG ? 1 : 2;
+    constexpr int PLANE = HALVES * kMuonPlane;
+    constexpr int STEP = BIG ? 16 : 32;                // columns of one step of the loading threads
+    constexpr int kIssueWarp = (kApplyLoad + kApplyDone) / 32;
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sq = smem;
     uint8_t* sv = smem + kApplyQ;
-    __shared__ __align__(8) uint64_t done[2], qfull[2], qfree[2];
+    __shared__ __align__(8) uint64_t vfull[2], vfree[2], ofull[2], ofree[2], qfull[2], qfree[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
-    __shared__ MuonMat record[4];   // matrix k's record in slot k & 3: at most three are in use at once
+    __shared__ MuonMat lrec[2];                        // the loading threads' matrices
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    float* stage = reinterpret_cast<float*>(smem + kApplyQ + kApplyV + warp * kApplyWarpStage);
     const int u0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x), u1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
     if (tid == 0) {
         for (int k = 0; k < 2; ++k) {
-            ptx::mbar_init(&done[k], 1);
+            ptx::mbar_init(&vfull[k], kApplyLoad / 32);
+            ptx::mbar_init(&vfree[k], 1);
+            ptx::mbar_init(&ofull[k], 1);
+            ptx::mbar_init(&ofree[k], kApplyDone / 32);
             ptx::mbar_init(&qfull[k], 1);
             ptx::mbar_init(&qfree[k], 1);
         }
         abort_flag = 0;
         ptx::fence_barrier_init();
     }
-    if (warp == 0) {
+    if (warp == kIssueWarp) {
         ptx::tmem_alloc<512>(&tmem_slot);
         ptx::tmem_relinquish();
     }
@@ -659,230 +1027,305 @@ muon_apply_kernel(const MuonMat* __restrict__ mats, int first, int last, int til
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const uint32_t sq0 = ptx::smem_u32(sq), sv0 = ptx::smem_u32(sv);
-    auto wait = [&](uint64_t* bar, uint32_t parity) { ptx::mbar_wait(bar, parity, &abort_flag, timeout_ns, err_flag); };
-
-    // state of the tile being loaded, of the one being multiplied and of the one being finished
+    auto wait = [&](uint64_t* bar, uint32_t parity) { ptx::mbar_wait_many(bar, parity, &abort_flag, timeout_ns, err_flag); };
     int mi = muon_find(first, last - 1, u0, [&](int k) { return mats[k].apply0; });
-    int row, x, rstep;
-    bool vec;
-    auto enter = [&]() {      // makes matrix mi the one whose tiles are loaded
-        muon_fetch(&record[mi & 3], mats + mi);
-        __syncthreads();
-        const MuonMat& M = record[mi & 3];
-        const int per = BIG ? 64 : 32;                 // quads of a tall tile's column
-        row = M.tall ? tid / per : tid >> 4;
-        x = M.tall ? tid % per : tid & 15;
-        rstep = M.tall ? kApplyThreads / per : kApplyThreads / 16;
-        vec = muon_aligned(M);
-    };
-    // rows 128 and up of a 256-row tile are short-side indices too
-    auto quad = [&](const MuonMat& Z, int tile, int i) {
-        if (!BIG) return muon_quad(Z, tile, row + i * rstep, x, 0, 64);
-        MuonQuad q{0, 0};
-        if (!Z.tall) {
-            const int c = row + i * rstep, l = tile * kMuonTileL + 4 * x;
-            if (c < Z.s) { q.n = max(0, min(4, Z.L - l)); q.e = c * Z.L + l; }
-        } else {
-            const int l = tile * kMuonTileL + row + i * rstep, c = 4 * x;
-            if (l < Z.L) { q.n = max(0, min(4, Z.s - c)); q.e = l * Z.s + c; }
-        }
-        return q;
-    };
-    float g[NQ][4], m[NQ][4];
-    auto load = [&](int u) {
-        const MuonMat& M = record[mi & 3];
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-            const MuonQuad q = quad(M, u - M.apply0, i);
-            muon_load4(M.g, q, vec, g[i]);
-            muon_load4(M.m, q, vec, m[i]);
-        }
-    };
-    int fin_mi = 0, fin_tile = 0;   // the finished tile
-    bool have = false;
-    uint32_t n_done = 0;        // tiles multiplied so far (buffer and parity of `done`)
-    uint32_t n_q = 0;           // Q pieces (BIG) or whole Qs loaded so far
-    const int quarter = warp & 3, cg = warp >> 2;       // this warp's accumulator rows and 16 columns
 
-    // the update of the finished tile from accumulator buffer `buf`
-    auto finish = [&](uint32_t buf) {
-        const MuonMat& fin = record[fin_mi & 3];
-        const float osc = fin.hdr[1];
+    if (warp < kApplyLoad / 32) {
+        // ------------------------------------------------------------ load
+        ptx::reg_inc<kApplyRegsLoad>();
+        using Tile = MuonTile<kApplyLoad, STEP, HALVES * 128>;
+        constexpr int STEPS = kMuonTileL / STEP;
+        Tile T;
+        auto enter = [&]() {      // makes matrix mi the one whose tiles are loaded
+            ptx::named_bar_sync(1, kApplyLoad);
+            if (tid < (int)(sizeof(MuonMat) / 8))
+                reinterpret_cast<uint64_t*>(&lrec[mi & 1])[tid] = reinterpret_cast<const uint64_t*>(mats + mi)[tid];
+            ptx::named_bar_sync(1, kApplyLoad);
+        };
+        enter();
+        T.enter(lrec[mi & 1], tid, true, 0, 64);
+        float g[Tile::NQ][4], m[Tile::NQ][4];
+        T.load(lrec[mi & 1], u0 - lrec[mi & 1].apply0, 0, g, m);
+        float xs = lrec[mi & 1].hdr[0];
+        int unclean = PLACES;     // places that may hold rows of a matrix with more of them
+        uint32_t k = 0;           // tiles so far
+        for (int u = u0; u < u1; ++u, ++k) {
+            const int slot = k % PLACES;
+            const uint32_t base = sv0 + slot * 3 * kMuonPlane;
+            const Tile S = T;     // this tile's matrix; T becomes the next one's
+            const MuonMat& C = lrec[mi & 1];
+            const float scale = xs;
+#pragma unroll 1
+            for (int st = 0; st < STEPS; ++st) {
+                float mn[Tile::NQ][4], x[Tile::NQ][4];
 #pragma unroll
-        for (int h = 0; h < HALVES; ++h) {
-            const int m0 = h * 128 + quarter * 32;      // first tile row of this warp
-            float p[16];
-            int at[16];
-            if (!fin.tall) {
+                for (int i = 0; i < Tile::NQ; ++i)
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const int mr = m0 + 2 * k + (lane >> 4);
-                    const int j = fin.J > 1 ? mr / fin.s : 0, c = mr - j * fin.s;
-                    const int l = (fin_tile * fin.J + j) * kMuonTileL + cg * 16 + (lane & 15);
-                    at[k] = (j < fin.J && c < fin.s && l < fin.L) ? c * fin.L + l : -1;
+                    for (int q = 0; q < 4; ++q) {
+                        mn[i][q] = muon_m(C, m[i][q], g[i][q]);
+                        x[i][q] = muon_u(C, mn[i][q], g[i][q]);
+                    }
+                if (st + 1 < STEPS) {
+                    T.load(C, u - C.apply0, (st + 1) * STEP, g, m);
+                } else if (u + 1 < u1) {
+                    if (u + 1 >= C.apply0 + C.tiles) {
+                        ++mi;
+                        enter();
+                        T.enter(lrec[mi & 1], tid, true, 0, 64);
+                        xs = lrec[mi & 1].hdr[0];
+                    }
+                    T.load(lrec[mi & 1], u + 1 - lrec[mi & 1].apply0, 0, g, m);
                 }
-            } else {
-                const int w = fin.J * fin.s, mr = m0 + lane;
-                const int total = fin.L * fin.s;
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const int e = (fin_tile * kMuonTileL + cg * 16 + k) * w + mr;
-                    at[k] = mr < w && e < total ? e : -1;
+                S.store(C, C.m, u - C.apply0, st * STEP, mn);
+                if (st == 0) {
+                    if (k >= PLACES) wait(&vfree[slot], ((k / PLACES) & 1u) ^ 1u);
+                    // rows past the matrix's are zero: their products reach no output, but must not be NaN
+                    if (unclean > 0) {
+                        for (int e = tid; e < 3 * PLANE / 16; e += kApplyLoad)
+                            reinterpret_cast<uint4*>(sv + slot * 3 * kMuonPlane)[e] = make_uint4(0, 0, 0, 0);
+                        ptx::named_bar_sync(1, kApplyLoad);
+                        --unclean;
+                    }
                 }
+                S.put(C, base, PLANE, st * STEP, scale, x);
             }
-#pragma unroll
-            for (int k = 0; k < 16; ++k) p[k] = at[k] >= 0 ? fin.p[at[k]] : 0.f;
-            if (h == 0) {
-                wait(&done[buf & 1], (buf >> 1) & 1u);
-                ptx::tc_fence_after();
-            }
-            const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16) + (buf & 1) * 256 + h * 128 + cg * 16;
-            uint32_t hi[16], lo[16];
+            if (u + 1 < u1 && u + 1 >= C.apply0 + C.tiles) unclean = PLACES;
+            ptx::fence_proxy_async_smem();
             __syncwarp();
-            ptx::tmem_ld16(t_row, hi);
-            ptx::tmem_ld16(t_row + 64, lo);
-            ptx::tmem_ld_wait();
-            float o[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = (__uint_as_float(hi[k]) + __uint_as_float(lo[k])) * osc;
-            if (!fin.tall) {
-                // rows of 16 consecutive elements: through shared memory, two rows per instruction
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < 16; ++k) stage[lane * 16 + (k ^ ((lane >> 1) & 15))] = o[k];
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const int r = 2 * k + (lane >> 4);
-                    o[k] = stage[r * 16 + ((lane & 15) ^ ((r >> 1) & 15))];
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                if (at[k] < 0) continue;
-                const float v = fmaf(-fin.step, o[k], p[k] * fin.decay);
-                fin.p[at[k]] = v;
-                if (fin.out) fin.out[at[k]] = __float2bfloat16_rn(v);
-            }
+            if (lane == 0) ptx::mbar_arrive(&vfull[slot]);
         }
-        ptx::tc_fence_before();
-    };
-
-    enter();
-    load(u0);
-    int mq = -1;                 // the matrix whose Q is in shared memory (or streamed)
-    for (int u = u0; u < u1; ++u) {
-        const int ci = mi;
-        const MuonMat& C = record[ci & 3];     // this tile's matrix
-        const int tile = u - C.apply0;
-        float xv[NQ][4];
-        const float xs = C.hdr[0];
-        const bool fresh = mq != mi;
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-            const MuonQuad q = quad(C, tile, i);
-            float mn[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                mn[k] = muon_m(C, m[i][k], g[i][k]);
-                xv[i][k] = muon_u(C, mn[k], g[i][k]) * xs;
+    } else if (warp < (kApplyLoad + kApplyDone) / 32) {
+        // ------------------------------------------------------------ finish
+        ptx::reg_dec<kApplyRegsDone>();
+        // A warp has 32 rows m (lanes) x 32 columns l' of O per half, in two blocks of 16 columns; through shared
+        // memory a block becomes quads of consecutive elements, four per lane (element by element where they
+        // are not aligned).  A block's p is requested before the block ahead of it is finished.
+        const int quarter = warp & 3, chalf = ((warp >> 2) & 1) * 32, ft = tid - kApplyLoad;
+        constexpr int BLOCKS = 2 * HALVES;
+        float* stage = reinterpret_cast<float*>(smem + kApplyQ + kApplyV + (ft >> 5) * kApplyBlock);
+        // what a block needs of its matrix; a tile's first block is entered while the last tile is finished
+        struct Mat {
+            float* p;
+            __nv_bfloat16* out;
+            int s, L, J, w, tall, apply0, end;
+            float decay, step, osc;
+        };
+        auto enter = [&](Mat& A, int i) {
+            const MuonMat& M = mats[i];
+            A.p = M.p;
+            A.out = M.out;
+            A.s = M.s;
+            A.L = M.L;
+            A.J = M.J;
+            A.w = M.J * M.s;
+            A.tall = M.tall;
+            A.apply0 = M.apply0;
+            A.end = M.apply0 + M.tiles;
+            A.decay = M.decay;
+            A.step = M.step;
+            A.osc = M.hdr[1];
+        };
+        auto aligned = [](const Mat& A) { return ((A.tall ? A.w : A.L) & 3) == 0; };
+        // first element of row r, column y of a tile; -1: none
+        auto place = [](const Mat& A, int tile, int r, int y) {
+            if (A.tall) {
+                const int e = (tile * kMuonTileL + y) * A.w + r;
+                return r < A.w && e < A.L * A.s ? e : -1;
             }
-            if (vec && q.n == 4) {
-                *reinterpret_cast<float4*>(C.m + q.e) = make_float4(mn[0], mn[1], mn[2], mn[3]);
-            } else {
+            int c = r, j = 0;
+            if (A.J > 1) { j = c / A.s; c -= j * A.s; }
+            const int l = (tile * A.J + j) * kMuonTileL + y;
+            return j < A.J && c < A.s && l < A.L ? c * A.L + l : -1;
+        };
+        float4 p[4];
+        int at[4];
+        auto request = [&](const Mat& A, int tile, int block) {
+            if (!aligned(A)) return;
+            const int m0 = (block >> 1) * 128 + quarter * 32, y0 = chalf + 16 * (block & 1);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k < q.n) C.m[q.e + k] = mn[k];
+            for (int i = 0; i < 4; ++i) {
+                at[i] = A.tall ? place(A, tile, m0 + (lane & 7) * 4, y0 + 4 * i + (lane >> 3))
+                               : place(A, tile, m0 + 8 * i + (lane >> 2), y0 + (lane & 3) * 4);
+                p[i] = at[i] >= 0 ? *reinterpret_cast<const float4*>(A.p + at[i]) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-        }
-        const int crow = row, cx = x, crstep = rstep;
-        // BIG: one tile buffer; otherwise the products that read this one ended before the previous finish
-        if (fresh || BIG) {
-            if (have) wait(&done[(n_done - 1) & 1], ((n_done - 1) >> 1) & 1u);
+        };
+        Mat A;
+        enter(A, mi);
+        request(A, u0 - A.apply0, 0);
+        uint32_t k = 0;
+        for (int u = u0; u < u1; ++u, ++k) {
+            const int tile = u - A.apply0;
+            wait(&ofull[k & 1], (k >> 1) & 1u);
             ptx::tc_fence_after();
-            __syncthreads();
-        }
-        if (fresh) {
-            if (!BIG && tid == 0) {
-                ptx::mbar_arrive_expect_tx(&qfull[0], kApplyQ);
-                ptx::bulk_load(sq, C.q, kApplyQ, &qfull[0]);
-            }
-            // rows past the matrix's are zero: their products reach no output, but must not be NaN
-            for (int e = tid; e < kApplyV / 16; e += kApplyThreads) reinterpret_cast<uint4*>(sv)[e] = make_uint4(0, 0, 0, 0);
-            __syncthreads();
-            mq = mi;
-        }
-        const uint32_t vbase = sv0 + (BIG ? 0u : (n_done & 1u) * (uint32_t)(3 * kMuonPlane));
+#pragma unroll 1
+            for (int b = 0; b < BLOCKS; ++b) {
+                const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16) + (k & 1) * 256 + (b >> 1) * 128 + chalf +
+                                       16 * (b & 1);
+                float o[16];
+                __syncwarp();
 #pragma unroll
-        for (int i = 0; i < NQ; ++i)
-            muon_split4(xv[i], vbase + muon_quad_at(C.tall, crow + i * crstep, cx), PLANE);
-        // the next tile's g and m
-        if (u + 1 < u1) {
-            if (u + 1 >= C.apply0 + C.tiles) {
-                ++mi;
-                enter();
-            }
-            load(u + 1);
-        }
-        ptx::fence_proxy_async_smem();
-        ptx::tc_fence_before();
-        __syncthreads();
-        ptx::tc_fence_after();
-        const uint32_t buf = n_done;
-        if (tid == 0) {
-            const uint32_t d0 = tmem + (buf & 1) * 256;
-            const uint32_t idesc = ptx::idesc_f16_f32(128, 64, false, !C.tall);
-            const int ksteps = (min(C.J * C.s, HALVES * 128) + 15) / 16;
-            // K step ks of the tile: its rows 16 ks ..
-            auto vdesc = [&](int ks) {
-                return C.tall ? ptx::smem_desc_sw128(vbase + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024)
-                              : ptx::smem_desc_sw128(vbase + ks * 2048, 8192, 1024);
-            };
-            if constexpr (!BIG) {
-                if (fresh) {
-                    wait(&qfull[0], n_q & 1u);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t hi[8], lo[8];
+                    ptx::tmem_ld8(t_row + 8 * h, hi);
+                    ptx::tmem_ld8(t_row + 64 + 8 * h, lo);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[8 * h + i] = (__uint_as_float(hi[i]) + __uint_as_float(lo[i])) * A.osc;
                 }
+                if (b == BLOCKS - 1) {        // the accumulators have been read
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&ofree[k & 1]);
+                }
+                float* const pp = A.p;
+                __nv_bfloat16* const po = A.out;
+                const float decay = A.decay, step = A.step;
+                const bool next = b + 1 < BLOCKS || u + 1 < u1;
+                auto request_next = [&]() {
+                    if (b + 1 < BLOCKS) {
+                        request(A, tile, b + 1);
+                    } else if (next) {
+                        if (u + 1 >= A.end) enter(A, ++mi);
+                        request(A, u + 1 - A.apply0, 0);
+                    }
+                };
+                if (!aligned(A)) {
+                    // tall: lanes are consecutive elements of a column; not tall: each lane its row
+                    const int e0 = place(A, tile, (b >> 1) * 128 + quarter * 32 + lane, chalf + 16 * (b & 1));
+                    const int d = A.tall ? A.w : 1;
+                    // (the matrix can end inside the block)
+                    const int n = e0 < 0 ? 0 : A.tall ? (A.L * A.s - e0 + A.w - 1) / A.w : A.L - e0 % A.L;
+#pragma unroll
+                    for (int h = 0; h < 16; h += 8) {
+                        float pv[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) pv[i] = h + i < n ? pp[e0 + (h + i) * d] : 0.f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (h + i < n) {
+                                const float v = fmaf(-step, o[h + i], pv[i] * decay);
+                                pp[e0 + (h + i) * d] = v;
+                                if (po) po[e0 + (h + i) * d] = __float2bfloat16_rn(v);
+                            }
+                    }
+                    request_next();
+                    continue;
+                }
+                const bool tall = A.tall != 0;
+                __syncwarp();
+                if (tall) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) stage[i * 32 + lane] = o[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<float4*>(stage + lane * 16 + ((i ^ (lane >> 1)) & 3) * 4) =
+                            make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+                __syncwarp();
+                float4 v[4];
+                int e[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 8 * i + (lane >> 2);
+                    const float4 q = *reinterpret_cast<const float4*>(
+                        tall ? stage + (4 * i + (lane >> 3)) * 32 + (lane & 7) * 4
+                             : stage + r * 16 + (((lane & 3) ^ (r >> 1)) & 3) * 4);
+                    v[i].x = fmaf(-step, q.x, p[i].x * decay);
+                    v[i].y = fmaf(-step, q.y, p[i].y * decay);
+                    v[i].z = fmaf(-step, q.z, p[i].z * decay);
+                    v[i].w = fmaf(-step, q.w, p[i].w * decay);
+                    e[i] = at[i];
+                }
+                request_next();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (e[i] < 0) continue;
+                    *reinterpret_cast<float4*>(pp + e[i]) = v[i];
+                    if (po) {
+                        const __nv_bfloat162 va = __floats2bfloat162_rn(v[i].x, v[i].y), vb = __floats2bfloat162_rn(v[i].z, v[i].w);
+                        *reinterpret_cast<uint2*>(po + e[i]) = make_uint2(*reinterpret_cast<const uint32_t*>(&va),
+                                                                         *reinterpret_cast<const uint32_t*>(&vb));
+                    }
+                }
+            }
+        }
+    } else {
+        ptx::reg_dec<kApplyRegsIssue>();
+    }
+    if (warp == kIssueWarp && lane == 0) {
+        // ------------------------------------------------------------ products
+        uint32_t k = 0, nq = 0;      // tiles, and Q pieces (BIG) or whole Qs, so far
+        int end = -1;                // first tile past the matrix
+        bool tall = false;
+        int ksteps = 0;
+        uint32_t idesc = 0;
+        const uint8_t* q = nullptr;
+        --mi;
+        for (int u = u0; u < u1; ++u, ++k) {
+            if (u >= end || k == 0) {
+                const MuonMat& M = mats[++mi];
+                end = M.apply0 + M.tiles;
+                tall = M.tall != 0;
+                ksteps = (min(M.J * M.s, HALVES * 128) + 15) / 16;
+                idesc = ptx::idesc_f16_f32(128, 64, false, !tall);
+                q = M.q;
+                if (!BIG) {
+                    if (k > 0) wait(&ofull[(k - 1) & 1], ((k - 1) >> 1) & 1u);   // the products that read the last Q
+                    ptx::mbar_arrive_expect_tx(&qfull[0], kApplyQ);
+                    ptx::bulk_load(sq, q, kApplyQ, &qfull[0]);
+                    wait(&qfull[0], nq & 1u);
+                    ++nq;
+                }
+            }
+            const int slot = k % PLACES;
+            const uint32_t vbase = sv0 + slot * 3 * kMuonPlane;
+            const uint32_t d0 = tmem + (k & 1) * 256;
+            // K step ks of the tile: its rows 16 ks ..
+            const uint64_t v0 = tall ? ptx::smem_desc_sw128(vbase, 16, 1024) : ptx::smem_desc_sw128(vbase, 8192, 1024);
+            auto vdesc = [&](int ks) {
+                return v0 + (tall ? (uint64_t)((ks >> 2) * 8192 + (ks & 3) * 32) / 16 : (uint64_t)ks * (2048 / 16));
+            };
+            wait(&vfull[slot], (k / PLACES) & 1u);
+            if (k >= 2) wait(&ofree[k & 1], ((k >> 1) & 1u) ^ 1u);
+            ptx::tc_fence_after();
+            if constexpr (!BIG) {
+                const uint64_t q0 = ptx::smem_desc_sw128(sq0, 16, 1024);
                 for (int ks = 0; ks < ksteps; ++ks)
-                    muon_mma(d0, d0 + 64, ptx::smem_desc_sw128(sq0 + (ks >> 2) * 3 * kMuonPlane + (ks & 3) * 32, 16, 1024),
-                             vdesc(ks), kMuonPlane / 16, PLANE / 16, idesc, ks == 0);
+                    muon_mma(d0, d0 + 64, q0 + (uint64_t)((ks >> 2) * 3 * kMuonPlane + (ks & 3) * 32) / 16, vdesc(ks),
+                             kMuonPlane / 16, PLANE / 16, idesc, ks == 0);
             } else {
                 const int kb = (ksteps + 3) / 4, pieces = 2 * kb;
-                auto fetch = [&](int k) {   // piece k: row half k / kb, column block k % kb
-                    const uint32_t nq = n_q + k;
-                    if (nq >= 2) wait(&qfree[nq & 1], ((nq >> 1) & 1u) ^ 1u);
-                    ptx::mbar_arrive_expect_tx(&qfull[nq & 1], 3 * kMuonPlane);
-                    ptx::bulk_load(sq + (nq & 1) * 3 * kMuonPlane, C.q + ((int64_t)(k / kb) * 4 + k % kb) * 3 * kMuonPlane,
-                                   3 * kMuonPlane, &qfull[nq & 1]);
+                auto fetch = [&](int c) {   // piece c: row half c / kb, column block c % kb
+                    const uint32_t n = nq + c;
+                    if (n >= 2) wait(&qfree[n & 1], ((n >> 1) & 1u) ^ 1u);
+                    ptx::mbar_arrive_expect_tx(&qfull[n & 1], 3 * kMuonPlane);
+                    ptx::bulk_load(sq + (n & 1) * 3 * kMuonPlane, q + ((int64_t)(c / kb) * 4 + c % kb) * 3 * kMuonPlane,
+                                   3 * kMuonPlane, &qfull[n & 1]);
                 };
                 fetch(0);
-                for (int k = 0; k < pieces; ++k) {
-                    if (k + 1 < pieces) fetch(k + 1);
-                    const uint32_t nq = n_q + k;
-                    wait(&qfull[nq & 1], (nq >> 1) & 1u);
-                    const int h = k / kb, b = k % kb;
+                for (int c = 0; c < pieces; ++c) {
+                    if (c + 1 < pieces) fetch(c + 1);
+                    const uint32_t n = nq + c;
+                    wait(&qfull[n & 1], (n >> 1) & 1u);
+                    const int h = c / kb, b = c % kb;
                     for (int ks = 0; ks < 4 && b * 4 + ks < ksteps; ++ks)
                         muon_mma(d0 + h * 128, d0 + h * 128 + 64,
-                                 ptx::smem_desc_sw128(sq0 + (nq & 1) * 3 * kMuonPlane + ks * 32, 16, 1024), vdesc(b * 4 + ks),
+                                 ptx::smem_desc_sw128(sq0 + (n & 1) * 3 * kMuonPlane + ks * 32, 16, 1024), vdesc(b * 4 + ks),
                                  kMuonPlane / 16, PLANE / 16, idesc, b == 0 && ks == 0);
-                    ptx::tc_commit(&qfree[nq & 1]);
+                    ptx::tc_commit(&qfree[n & 1]);
                 }
-                n_q += pieces;
+                nq += pieces;
             }
-            ptx::tc_commit(&done[buf & 1]);
+            ptx::tc_commit(&vfree[slot]);
+            ptx::tc_commit(&ofull[k & 1]);
         }
-        if (!BIG && fresh) ++n_q;
-        __syncwarp();
-        ++n_done;
-        if (have) finish(buf - 1);
-        fin_mi = ci;
-        fin_tile = tile;
-        have = true;
     }
-    if (have) finish(n_done - 1);
+    __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (warp == 0) ptx::tmem_dealloc<512>(tmem);
+    if (warp == kIssueWarp) ptx::tmem_dealloc<512>(tmem);
 }
 
 }  // namespace plora

@@ -1611,12 +1611,14 @@ void muon_plan(const plora_ctx* h, int32_t n, const plora_adapter* tab, MuonPlan
             M.tall = p.rows > p.cols;
             M.J = M.s <= 64 ? 128 / M.s : 1;
             M.tiles = (int32_t)ceil_div(M.L, (int64_t)kMuonTileL * M.J);
-            M.nchunks = (int32_t)ceil_div(M.tiles, kMuonGramTiles);
+            // 16 chunks, of at least 8 tiles (a chunk's partial is read again) and at most 16
+            M.per_chunk = (int32_t)std::min<int64_t>(kGramExactTiles, std::max<int64_t>(8, ceil_div(M.tiles, 16)));
+            M.nchunks = (int32_t)ceil_div(M.tiles, M.per_chunk);
             const int32_t ng = (int32_t)ceil_div(M.s, 64);
             M.npairs = ng <= 2 ? 1 : ng * (ng - 1) / 2;
             const size_t s2 = (size_t)M.s * (size_t)M.s, sp = (size_t)round_up(M.s, 8);
             p.part = take(s2 * (size_t)M.nchunks * sizeof(double));
-            p.ns = take(4 * sp * sp * sizeof(double));
+            if (M.s > kNsSmallS) p.ns = take(5 * sp * sp * sizeof(double));
             p.q = take((size_t)(big ? 24 : 6) * kMuonPlane);
             p.hdr = take((size_t)(2 + M.nchunks * M.npairs + kMuonCluster) * sizeof(float));
             M.gram0 = (int32_t)P.gram_items;
@@ -1717,9 +1719,16 @@ plora_status muon_step(plora_ctx* h, int32_t n, const plora_adapter* tab, const 
         M.steps = o.ns_steps;
         M.nesterov = o.nesterov;
     }
-    uint8_t *dm = nullptr, *none = nullptr;
+    uint8_t *dm = nullptr, *dorder = nullptr;
     int slot = 0;
-    s = upload_parts(h, P.mats.data(), P.mats.size() * sizeof(MuonMat), nullptr, 0, cs, &dm, &none, &slot);
+    // the iteration's order: matrices that take a cluster first, the largest first
+    std::vector<int32_t> order(P.mats.size());
+    for (size_t k = 0; k < order.size(); ++k) order[k] = (int32_t)k;
+    std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return P.mats[x].s > P.mats[y].s; });
+    int n_cluster = 0;
+    for (const MuonMat& M : P.mats) n_cluster += M.s > kNsSmallS ? 1 : 0;
+    s = upload_parts(h, P.mats.data(), P.mats.size() * sizeof(MuonMat), order.data(), order.size() * sizeof(int32_t), cs,
+                     &dm, &dorder, &slot);
     if (s != PLORA_OK) return s;
     const MuonMat* mats = reinterpret_cast<const MuonMat*>(dm);
     const int nm = (int)P.mats.size();
@@ -1727,7 +1736,21 @@ plora_status muon_step(plora_ctx* h, int32_t n, const plora_adapter* tab, const 
     tracked(h, kMuonGramK, cs, [&] {
         muon_gram_kernel<<<(unsigned)P.gram_items, kGramThreads, kGramSmem, cs>>>(mats, nm, err, kTimeoutNs);
     });
-    tracked(h, kMuonNsK, cs, [&] { muon_ns_kernel<<<(unsigned)nm * kMuonCluster, 256, kMuonNsSmem, cs>>>(mats); });
+    const int clusters = n_cluster + (int)ceil_div(nm - n_cluster, kMuonCluster);
+    tracked(h, kMuonNsK, cs, [&] {
+        // clusters spread over the SMs rather than two blocks of one cluster sharing an SM
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterSchedulingPolicyPreference;
+        attr[0].val.clusterSchedulingPolicyPreference = cudaClusterSchedulingPolicySpread;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)clusters * kMuonCluster);
+        cfg.blockDim = dim3(256);
+        cfg.dynamicSmemBytes = kMuonNsSmem;
+        cfg.stream = cs;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        cudaLaunchKernelEx(&cfg, muon_ns_kernel, mats, (const int32_t*)dorder, n_cluster, nm);
+    });
     const int32_t ns = P.n_small;
     if (ns > 0)
         tracked(h, kMuonApplyK, cs, [&] {
@@ -1851,7 +1874,8 @@ plora_status plora_create(plora_handle* out, const plora_config* cfg) {
                                                 (size_t)round_up(adamw_chunks * (int64_t)sizeof(AdamwChunk), 256) +
                                                 1024);
     // So does the Muon step's table, two matrices per adapter and output block.
-    h->blob_bytes = std::max(h->blob_bytes, (size_t)round_up(2 * na * nblk * (int64_t)sizeof(MuonMat), 256) + 1024);
+    h->blob_bytes = std::max(h->blob_bytes, (size_t)round_up(2 * na * nblk * (int64_t)sizeof(MuonMat), 256) +
+                                                (size_t)round_up(2 * na * nblk * (int64_t)sizeof(int32_t), 256) + 1024);
 
     size_t o = 0;
     auto carve = [&](Region& r, size_t bytes) {
