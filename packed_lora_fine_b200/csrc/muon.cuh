@@ -97,20 +97,25 @@ __device__ __forceinline__ uint32_t muon_elem_at(int row, int y) {
            (uint32_t)(y & 7) * 2u;
 }
 
-// v = x0 + x1 + x2 (see the top of the file).  |v| <= 256, so adding 1.5 2^23 rounds to an integer.
-__device__ __forceinline__ void muon_split2(float a, float b, uint32_t (&h)[3]) {
+// scale * v = x0 + x1 + x2 (see the top of the file), two values at a time.  |scale v| <= 256, so adding
+// 1.5 2^23 rounds to an integer; scale is a power of two, so the products are exact.
+__device__ __forceinline__ void muon_split2(uint64_t v, uint64_t scale, uint32_t (&h)[3]) {
     constexpr float kRound = 12582912.f;
-    const float a0 = __fadd_rn(__fadd_rn(a, kRound), -kRound), b0 = __fadd_rn(__fadd_rn(b, kRound), -kRound);
-    const float ra = a - a0, rb = b - b0;
-    const __half2 h0 = __floats2half2_rn(a0, b0), h1 = __floats2half2_rn(ra, rb);
+    const uint64_t round = ptx::f32x2(kRound, kRound), neg = ptx::f32x2(-1.f, -1.f);
+    const uint64_t t = ptx::f32x2_fma(v, scale, round);             // x0 + 1.5 2^23
+    const uint64_t n0 = ptx::f32x2_fma(t, neg, round);              // -x0
+    const uint64_t r = ptx::f32x2_fma(v, scale, n0);
+    const float2 x0 = ptx::f32x2_get(ptx::f32x2_add(t, ptx::f32x2(-kRound, -kRound))), rr = ptx::f32x2_get(r);
+    const __half2 h0 = __floats2half2_rn(x0.x, x0.y), h1 = __floats2half2_rn(rr.x, rr.y);
     const float2 f1 = __half22float2(h1);
-    const __half2 h2 = __floats2half2_rn(ra - f1.x, rb - f1.y);
+    const float2 x2 = ptx::f32x2_get(ptx::f32x2_fma(ptx::f32x2(f1.x, f1.y), neg, r));
+    const __half2 h2 = __floats2half2_rn(x2.x, x2.y);
     h[0] = *reinterpret_cast<const uint32_t*>(&h0);
     h[1] = *reinterpret_cast<const uint32_t*>(&h1);
     h[2] = *reinterpret_cast<const uint32_t*>(&h2);
 }
 
-// How T threads hold a step of TL columns of a tile of ROWS rows, 16 elements each, in the order of memory:
+// How T threads hold a step of TL columns of a tile of ROWS rows, 4 NQ elements each, in the order of memory:
 //   kRows    not tall, L % 4 == 0: quads of 4 columns of a row
 //   kFlat    tall, w = J s a multiple of 4: quads of the step's TL w consecutive elements
 //   kPairs   tall, other w: pairs of consecutive rows m of a column l'
@@ -120,7 +125,6 @@ template <int T, int TL, int ROWS>
 struct MuonTile {
     enum { kRows, kFlat, kPairs, kQuads };
     static constexpr int NQ = ROWS * TL / 4 / T;
-    static_assert(NQ == 4, "16 elements per thread");
     static constexpr int kPairCols = T / (ROWS / 2);   // columns l' that the threads' pairs cover at once
     static constexpr int kRowStep = T / (TL / 4);      // rows that the threads' quads cover at once (not tall)
     static constexpr int kColStep = T / (ROWS / 4);    // columns that the threads' quads cover at once (tall)
@@ -227,8 +231,8 @@ struct MuonTile {
         const float *pg = M.g, *pm = M.m;
         uint8_t* const rm = raw + NQ * T * 16;
         auto quads = [&](int i, int e, bool ok) {
-            ptx::cp_async16(raw + i * T * 16, ok ? pg + e : pg, ok ? 16 : 0);
-            ptx::cp_async16(rm + i * T * 16, ok ? pm + e : pm, ok ? 16 : 0);
+            ptx::cp_async16(ptx::smem_u32(raw) + i * T * 16, ok ? pg + e : pg, ok ? 16 : 0);
+            ptx::cp_async16(ptx::smem_u32(rm) + i * T * 16, ok ? pm + e : pm, ok ? 16 : 0);
         };
         auto single = [&](int i, int k, int e, bool ok) {
             ptx::cp_async4(ptx::smem_u32(raw) + i * T * 16 + k * 4, ok ? pg + e : pg, ok ? 4 : 0);
@@ -309,11 +313,12 @@ struct MuonTile {
     // zeros; rows past the matrix's are left alone.
     __device__ __forceinline__ void put(const MuonMat& M, uint32_t base, uint32_t plane, int col0, float scale,
                                         const float (&v)[NQ][4]) const {
+        const uint64_t scale2 = ptx::f32x2(scale, scale);
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
             uint32_t a[3], b[3];
-            muon_split2(v[i][0] * scale, v[i][1] * scale, a);
-            muon_split2(v[i][2] * scale, v[i][3] * scale, b);
+            muon_split2(ptx::f32x2(v[i][0], v[i][1]), scale2, a);
+            muon_split2(ptx::f32x2(v[i][2], v[i][3]), scale2, b);
             if (mode == kPairs) {
                 if (x < M.J * M.s) {
                     const uint32_t aa = base + muon_elem_at(col0 + row + 2 * i * kPairCols, x);
@@ -341,17 +346,26 @@ struct MuonTile {
 };
 
 // D0 += a0 b0, D1 += the products of a lower order, over one K step; the parts of an operand lie
-// `astep` / `bstep` (in descriptor units of 16 bytes) apart.
-__device__ __forceinline__ void muon_mma(uint32_t d0, uint32_t d1, uint64_t a, uint64_t b, uint64_t astep, uint64_t bstep,
-                                         uint32_t idesc, bool first) {
-    ptx::tc_mma_f16(d0, a, b, idesc, first ? 0u : 1u);
-    ptx::tc_mma_f16(d1, a, b + bstep, idesc, first ? 0u : 1u);
-    ptx::tc_mma_f16(d1, a + astep, b, idesc, 1u);
-    ptx::tc_mma_f16(d1, a + astep, b + bstep, idesc, 1u);
-    ptx::tc_mma_f16(d1, a, b + 2 * bstep, idesc, 1u);
-    ptx::tc_mma_f16(d1, a + 2 * astep, b, idesc, 1u);
-    ptx::tc_mma_f16(d1, a + astep, b + 2 * bstep, idesc, 1u);
-    ptx::tc_mma_f16(d1, a + 2 * astep, b + bstep, idesc, 1u);
+// `astep` / `bstep` (in descriptor units of 16 bytes) apart.  FIRST: the products start the accumulators.
+// ALL: x1 x2 and x2 x1 too, 2^-26 of the largest product each: G needs them (its error grows with the iteration),
+// Q X_0 does not.
+struct MuonDesc {
+    uint32_t lo, hi;
+    __device__ __forceinline__ MuonDesc(uint64_t d) : lo((uint32_t)d), hi((uint32_t)(d >> 32)) {}
+};
+template <bool FIRST, bool ALL>
+__device__ __forceinline__ void muon_mma(uint32_t d0, uint32_t d1, MuonDesc a, MuonDesc b, uint32_t astep, uint32_t bstep,
+                                         uint32_t idesc) {
+    ptx::tc_mma_f16_lo<!FIRST>(d0, a.lo, a.hi, b.lo, b.hi, idesc);
+    ptx::tc_mma_f16_lo<!FIRST>(d1, a.lo, a.hi, b.lo + bstep, b.hi, idesc);
+    ptx::tc_mma_f16_lo<true>(d1, a.lo + astep, a.hi, b.lo, b.hi, idesc);
+    ptx::tc_mma_f16_lo<true>(d1, a.lo + astep, a.hi, b.lo + bstep, b.hi, idesc);
+    ptx::tc_mma_f16_lo<true>(d1, a.lo, a.hi, b.lo + 2 * bstep, b.hi, idesc);
+    ptx::tc_mma_f16_lo<true>(d1, a.lo + 2 * astep, a.hi, b.lo, b.hi, idesc);
+    if constexpr (ALL) {
+        ptx::tc_mma_f16_lo<true>(d1, a.lo + astep, a.hi, b.lo + 2 * bstep, b.hi, idesc);
+        ptx::tc_mma_f16_lo<true>(d1, a.lo + 2 * astep, a.hi, b.lo + bstep, b.hi, idesc);
+    }
 }
 
 // ---------------------------------------------------------------------------------------------- Gram
@@ -601,12 +615,15 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
             if (todo == kStop) break;
             ptx::tc_fence_after();
             const uint32_t base = s0 + place * kGramStage;
-            const uint64_t kstep = tall ? 2048 / 16 : 32 / 16;
-            const uint64_t d = tall ? ptx::smem_desc_sw128(base, 8192, 1024) : ptx::smem_desc_sw128(base, 16, 1024);
+            const uint32_t kstep = tall ? 2048 / 16 : 32 / 16;
+            MuonDesc d = tall ? ptx::smem_desc_sw128(base, 8192, 1024) : ptx::smem_desc_sw128(base, 16, 1024);
+            if (todo == kStart) muon_mma<true, true>(tmem, tmem + 128, d, d, kMuonPlane / 16, kMuonPlane / 16, idesc);
+            else muon_mma<false, true>(tmem, tmem + 128, d, d, kMuonPlane / 16, kMuonPlane / 16, idesc);
 #pragma unroll
-            for (int q = 0; q < kMuonTileL / 16; ++q)
-                muon_mma(tmem, tmem + 128, d + q * kstep, d + q * kstep, kMuonPlane / 16, kMuonPlane / 16, idesc,
-                         todo == kStart && q == 0);
+            for (int q = 1; q < kMuonTileL / 16; ++q) {
+                d.lo += kstep;
+                muon_mma<false, true>(tmem, tmem + 128, d, d, kMuonPlane / 16, kMuonPlane / 16, idesc);
+            }
             ptx::tc_commit(&done[place]);
         }
     }
@@ -682,12 +699,12 @@ __device__ __forceinline__ void ns_products(const NsProduct& p0, const NsProduct
             const bool kin = k0 < sp;
             const double* a = p.A + (kin ? ra * sp + k0 : 0);
             const double* b = p.B + (kin ? rb * sp + k0 : 0);
-            double* dst = sm + fc.st * kNsStageD + frow * kNsPitch + fcol;
+            const uint32_t dst = ptx::smem_u32(sm + fc.st * kNsStageD + frow * kNsPitch + fcol);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const bool ia = kin && ra + 8 * i < sp, ib = kin && rb + 8 * i < sp;
-                ptx::cp_async16(dst + 8 * i * kNsPitch, ia ? a + 8 * i * sp : p.A, ia ? 16 : 0);
-                ptx::cp_async16(dst + (T + 8 * i) * kNsPitch, ib ? b + 8 * i * sp : p.B, ib ? 16 : 0);
+                ptx::cp_async16(dst + 8 * i * kNsPitch * 8, ia ? a + 8 * i * sp : p.A, ia ? 16 : 0);
+                ptx::cp_async16(dst + (T + 8 * i) * kNsPitch * 8, ib ? b + 8 * i * sp : p.B, ib ? 16 : 0);
             }
             next(fc);
         }
@@ -969,17 +986,14 @@ muon_ns_kernel(const MuonMat* __restrict__ mats, const int32_t* __restrict__ ord
 }
 
 // --------------------------------------------------------------------------------------------- apply
-constexpr int kApplyLoad = 256;                       // threads that load, split and store m: warps 0 .. 7
-constexpr int kApplyDone = 256;                       // threads that finish p: warps 8 .. 15
-constexpr int kApplyThreads = kApplyLoad + kApplyDone + 128;  // and a warpgroup whose first warp issues the products
-// Registers per thread of the three; the launch has kApplyThreads x 96 (640 threads).
-constexpr int kApplyRegsLoad = 128, kApplyRegsDone = 80, kApplyRegsIssue = 40;
-static_assert(kApplyLoad * kApplyRegsLoad + kApplyDone * kApplyRegsDone + 128 * kApplyRegsIssue <= kApplyThreads * 96,
-              "register shares");
+constexpr int kApplyLoad = 512;                       // threads that load, split and store m: warps 0 .. 15
+constexpr int kApplyDone = 256;                       // threads that finish p: warps 16 .. 23
+constexpr int kApplyThreads = kApplyLoad + kApplyDone + 32;   // and a warp that issues the products
+constexpr int kApplyAhead = 2;                        // tiles whose lines are brought to L2 ahead
 constexpr int kApplyQ = 6 * kMuonPlane;               // Q of s <= 128, or two (half, column block) pieces
 constexpr int kApplyV = 6 * kMuonPlane;               // two tiles of 128 rows, or one of 256
-constexpr int kApplyBlock = 32 * 16 * 4;              // a finishing warp's 32 x 16 block of O
-constexpr int kApplySmem = kApplyQ + kApplyV + (kApplyDone / 32) * kApplyBlock + 1024;
+constexpr int kApplyBlock = 32 * 16 * 4;              // a finishing warp's 32 x 16 block of p, in two places
+constexpr int kApplySmem = kApplyQ + kApplyV + (kApplyDone / 32) * 2 * kApplyBlock + 1024;
 static_assert(kApplySmem + 1024 <= 232448, "shared memory per CTA");
 
 // O = Q X_0 tile by tile, then p, its bf16 copy and m.  One block per SM over a contiguous run of tiles (all
@@ -987,7 +1001,7 @@ static_assert(kApplySmem + 1024 <= 232448, "shared memory per CTA");
 //   load     g and m of a step (the next step's are on their way), m <- the new m, u in parts to shared memory
 //   products Q, kept in shared memory while the matrix lasts, times the tile: 64 columns of O in two
 //            accumulators, of two such sets in turn
-//   finish   p (requested before O is there), O out of the accumulators, the new p and its bf16 copy
+//   finish   p to shared memory (two blocks ahead), O out of the accumulators onto it, the new p and its copy
 // BIG (s > 128): tiles of 256 rows in one place, Q's (row half, column block) pieces streamed from L2.
 template <bool BIG>
 __global__ void __launch_bounds__(kApplyThreads, 1)
@@ -1003,7 +1017,7 @@ muon_apply_kernel(const MuonMat* __restrict__ mats, int first, int last, int til
     __shared__ __align__(8) uint64_t vfull[2], vfree[2], ofull[2], ofree[2], qfull[2], qfree[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
-    __shared__ MuonMat lrec[2];                        // the loading threads' matrices
+    __shared__ MuonMat lrec[2], frec[2];               // the loading and the finishing threads' matrices
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int u0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x), u1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
     if (tid == 0) {
@@ -1032,7 +1046,6 @@ muon_apply_kernel(const MuonMat* __restrict__ mats, int first, int last, int til
 
     if (warp < kApplyLoad / 32) {
         // ------------------------------------------------------------ load
-        ptx::reg_inc<kApplyRegsLoad>();
         using Tile = MuonTile<kApplyLoad, STEP, HALVES * 128>;
         constexpr int STEPS = kMuonTileL / STEP;
         Tile T;
@@ -1044,39 +1057,60 @@ muon_apply_kernel(const MuonMat* __restrict__ mats, int first, int last, int til
         };
         enter();
         T.enter(lrec[mi & 1], tid, true, 0, 64);
-        float g[Tile::NQ][4], m[Tile::NQ][4];
-        T.load(lrec[mi & 1], u0 - lrec[mi & 1].apply0, 0, g, m);
+        // This thread's 128-byte line of a tile's g, m and p in tile 0 (BIG: and a second one): they are brought to
+        // L2 two tiles ahead, so that the loads, whose number in flight registers limit, wait for L2 alone.
+        int line = -1, line2 = 0;
+        auto enter_line = [&](const MuonMat& M) {
+            if (M.tall) {
+                line = (tid & 255) * 32 < kMuonTileL * M.J * M.s ? (tid & 255) * 32 : -1;
+                line2 = 256 * 32;
+            } else {
+                const int r = (tid & 255) >> 1, j = M.J > 1 ? r / M.s : 0, c = r - j * M.s;
+                line = j < M.J && c < M.s ? c * M.L + j * kMuonTileL + (tid & 1) * 32 : -1;
+                line2 = 128 * M.L;
+            }
+        };
+        auto prefetch = [&](const MuonMat& M, int tile) {
+            if (tile >= M.tiles || line < 0) return;
+            const int total = M.L * M.s, e = line + tile * kMuonTileL * (M.tall ? M.J * M.s : M.J);
+#pragma unroll
+            for (int k = 0; k < HALVES; ++k) {
+                if (e + k * line2 >= total || (k && M.tall && line + line2 >= kMuonTileL * M.s)) break;
+                ptx::prefetch_l2(M.g + e + k * line2);
+                ptx::prefetch_l2(M.m + e + k * line2);
+                ptx::prefetch_l2(M.p + e + k * line2);
+            }
+        };
+        enter_line(lrec[mi & 1]);
         float xs = lrec[mi & 1].hdr[0];
         int unclean = PLACES;     // places that may hold rows of a matrix with more of them
         uint32_t k = 0;           // tiles so far
         for (int u = u0; u < u1; ++u, ++k) {
             const int slot = k % PLACES;
             const uint32_t base = sv0 + slot * 3 * kMuonPlane;
-            const Tile S = T;     // this tile's matrix; T becomes the next one's
             const MuonMat& C = lrec[mi & 1];
-            const float scale = xs;
+            const int tile = u - C.apply0;
+            const bool last_of = tile + 1 == C.tiles;      // the next tile is another matrix's
+            const uint64_t mu2 = ptx::f32x2(C.mu, C.mu);
+            const bool nesterov = C.nesterov != 0;
+            if (tid < 256 && u + kApplyAhead < u1) prefetch(C, tile + kApplyAhead);
 #pragma unroll 1
             for (int st = 0; st < STEPS; ++st) {
-                float mn[Tile::NQ][4], x[Tile::NQ][4];
+                float g[Tile::NQ][4], m[Tile::NQ][4];
+                T.load(C, tile, st * STEP, g, m);
 #pragma unroll
                 for (int i = 0; i < Tile::NQ; ++i)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        mn[i][q] = muon_m(C, m[i][q], g[i][q]);
-                        x[i][q] = muon_u(C, mn[i][q], g[i][q]);
+                    for (int q = 0; q < 4; q += 2) {
+                        const uint64_t gg = ptx::f32x2(g[i][q], g[i][q + 1]);
+                        const uint64_t a = ptx::f32x2_fma(mu2, ptx::f32x2(m[i][q], m[i][q + 1]), gg);
+                        const float2 b = ptx::f32x2_get(a), c = ptx::f32x2_get(nesterov ? ptx::f32x2_fma(mu2, a, gg) : a);
+                        m[i][q] = b.x;
+                        m[i][q + 1] = b.y;
+                        g[i][q] = c.x;
+                        g[i][q + 1] = c.y;
                     }
-                if (st + 1 < STEPS) {
-                    T.load(C, u - C.apply0, (st + 1) * STEP, g, m);
-                } else if (u + 1 < u1) {
-                    if (u + 1 >= C.apply0 + C.tiles) {
-                        ++mi;
-                        enter();
-                        T.enter(lrec[mi & 1], tid, true, 0, 64);
-                        xs = lrec[mi & 1].hdr[0];
-                    }
-                    T.load(lrec[mi & 1], u + 1 - lrec[mi & 1].apply0, 0, g, m);
-                }
-                S.store(C, C.m, u - C.apply0, st * STEP, mn);
+                T.store(C, C.m, tile, st * STEP, m);
                 if (st == 0) {
                     if (k >= PLACES) wait(&vfree[slot], ((k / PLACES) & 1u) ^ 1u);
                     // rows past the matrix's are zero: their products reach no output, but must not be NaN
@@ -1087,174 +1121,204 @@ muon_apply_kernel(const MuonMat* __restrict__ mats, int first, int last, int til
                         --unclean;
                     }
                 }
-                S.put(C, base, PLANE, st * STEP, scale, x);
+                T.put(C, base, PLANE, st * STEP, xs, g);
             }
-            if (u + 1 < u1 && u + 1 >= C.apply0 + C.tiles) unclean = PLACES;
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&vfull[slot]);
+            if (u + 1 < u1 && last_of) {
+                unclean = PLACES;
+                ++mi;
+                enter();
+                T.enter(lrec[mi & 1], tid, true, 0, 64);
+                enter_line(lrec[mi & 1]);
+                xs = lrec[mi & 1].hdr[0];
+            }
         }
     } else if (warp < (kApplyLoad + kApplyDone) / 32) {
         // ------------------------------------------------------------ finish
-        ptx::reg_dec<kApplyRegsDone>();
-        // A warp has 32 rows m (lanes) x 32 columns l' of O per half, in two blocks of 16 columns; through shared
-        // memory a block becomes quads of consecutive elements, four per lane (element by element where they
-        // are not aligned).  A block's p is requested before the block ahead of it is finished.
+        // A warp has 32 rows m (lanes) x 32 columns l' per half of the tile, in blocks of 32 x 16.  p comes to
+        // shared memory as quads of consecutive elements (four per lane), takes scale O row by row, and
+        // leaves as quads again.  A quad's cell of a block: tall [column][row], otherwise [row][column], swizzled.
         const int quarter = warp & 3, chalf = ((warp >> 2) & 1) * 32, ft = tid - kApplyLoad;
         constexpr int BLOCKS = 2 * HALVES;
-        float* stage = reinterpret_cast<float*>(smem + kApplyQ + kApplyV + (ft >> 5) * kApplyBlock);
-        // what a block needs of its matrix; a tile's first block is entered while the last tile is finished
-        struct Mat {
-            float* p;
-            __nv_bfloat16* out;
-            int s, L, J, w, tall, apply0, end;
-            float decay, step, osc;
+        float* const places = reinterpret_cast<float*>(smem + kApplyQ + kApplyV + (ft >> 5) * 2 * kApplyBlock);
+        auto enter = [&](int i) {
+            ptx::named_bar_sync(2, kApplyDone);
+            if (ft < (int)(sizeof(MuonMat) / 8))
+                reinterpret_cast<uint64_t*>(&frec[i & 1])[ft] = reinterpret_cast<const uint64_t*>(mats + i)[ft];
+            ptx::named_bar_sync(2, kApplyDone);
         };
-        auto enter = [&](Mat& A, int i) {
-            const MuonMat& M = mats[i];
-            A.p = M.p;
-            A.out = M.out;
-            A.s = M.s;
-            A.L = M.L;
-            A.J = M.J;
-            A.w = M.J * M.s;
-            A.tall = M.tall;
-            A.apply0 = M.apply0;
-            A.end = M.apply0 + M.tiles;
-            A.decay = M.decay;
-            A.step = M.step;
-            A.osc = M.hdr[1];
+        // this lane's quad i of block b of a tile: its first element and how many exist
+        struct First {
+            int e[4];      // of a tile's first block in tile 0; -1: rows past the matrix's
         };
-        auto aligned = [](const Mat& A) { return ((A.tall ? A.w : A.L) & 3) == 0; };
-        // first element of row r, column y of a tile; -1: none
-        auto place = [](const Mat& A, int tile, int r, int y) {
-            if (A.tall) {
-                const int e = (tile * kMuonTileL + y) * A.w + r;
-                return r < A.w && e < A.L * A.s ? e : -1;
-            }
-            int c = r, j = 0;
-            if (A.J > 1) { j = c / A.s; c -= j * A.s; }
-            const int l = (tile * A.J + j) * kMuonTileL + y;
-            return j < A.J && c < A.s && l < A.L ? c * A.L + l : -1;
-        };
-        float4 p[4];
-        int at[4];
-        auto request = [&](const Mat& A, int tile, int block) {
-            if (!aligned(A)) return;
-            const int m0 = (block >> 1) * 128 + quarter * 32, y0 = chalf + 16 * (block & 1);
+        auto quad_row = [&](bool tall, int i) { return quarter * 32 + (tall ? (lane & 7) * 4 : 8 * i + (lane >> 2)); };
+        auto quad_col = [&](bool tall, int i) { return chalf + (tall ? 4 * i + (lane >> 3) : (lane & 3) * 4); };
+        auto first_of = [&](const MuonMat& M) {
+            First f;
+            const bool tall = M.tall != 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                at[i] = A.tall ? place(A, tile, m0 + (lane & 7) * 4, y0 + 4 * i + (lane >> 3))
-                               : place(A, tile, m0 + 8 * i + (lane >> 2), y0 + (lane & 3) * 4);
-                p[i] = at[i] >= 0 ? *reinterpret_cast<const float4*>(A.p + at[i]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const int r = quad_row(tall, i), y = quad_col(tall, i);
+                if (tall) {
+                    f.e[i] = r < M.J * M.s ? y * M.J * M.s + r : -1;
+                } else {
+                    const int j = M.J > 1 ? r / M.s : 0, c = r - j * M.s;
+                    f.e[i] = j < M.J && c < M.s ? c * M.L + j * kMuonTileL + y : -1;
+                }
             }
+            return f;
         };
-        Mat A;
-        enter(A, mi);
-        request(A, u0 - A.apply0, 0);
-        uint32_t k = 0;
+        auto quad = [&](const MuonMat& M, const First& f, int tile, int b, int i, int& n) {
+            const bool tall = M.tall != 0;
+            const int y0 = 16 * (b & 1), m0 = (b >> 1) * 128, w = M.J * M.s;
+            const int e = f.e[i] + (tall ? (tile * kMuonTileL + y0) * w + m0 : tile * kMuonTileL * M.J + y0 + m0 * M.L);
+            n = f.e[i] >= 0 ? 4 : 0;
+            if (BIG && b >= 2 && quad_row(tall, i) + 128 >= M.s) n = 0;
+            if (tall) {
+                n = min(n, w - m0 - quad_row(true, i));
+                if (tile + 1 >= M.tiles) n = min(n, M.L * M.s - e);
+            } else if (tile + 1 >= M.tiles) {
+                const int r = quad_row(false, i), j = M.J > 1 ? r / M.s : 0;
+                n = min(n, M.L - (tile * M.J + j) * kMuonTileL - y0 - quad_col(false, i));
+            }
+            return e;
+        };
+        auto aligned = [](const MuonMat& M) { return ((M.tall ? M.J * M.s : M.L) & 3) == 0; };
+        auto cell = [&](bool tall, int i) {
+            const int r = 8 * i + (lane >> 2);
+            return tall ? (4 * i + (lane >> 3)) * 32 + (lane & 7) * 4 : r * 16 + (((lane & 3) ^ (r >> 1)) & 3) * 4;
+        };
+        // the cursor of the blocks that are fetched
+        int fu = u0, fb = 0, fmi = mi;
+        uint32_t fseq = 0;
+        enter(mi);
+        First ff = first_of(frec[mi & 1]), pf = ff;
+        int end = frec[mi & 1].apply0 + frec[mi & 1].tiles;      // of the matrix being finished
+        // (The next matrix is entered when its first block is fetched: by then a block of the tile ahead of it has
+        // been finished, so a matrix two before it, whose record it replaces, is behind every warp.)
+        int fend = end;
+        auto fetch = [&]() {
+            if (fu < u1) {
+                if (fu == fend) {
+                    enter(++fmi);
+                    ff = first_of(frec[fmi & 1]);
+                    fend = frec[fmi & 1].apply0 + frec[fmi & 1].tiles;
+                }
+                const MuonMat& M = frec[fmi & 1];
+                const uint32_t at = ptx::smem_u32(places) + (fseq & 1) * kApplyBlock;
+                const bool vec = aligned(M), tall = M.tall != 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    int n;
+                    const int e = quad(M, ff, fu - M.apply0, fb, i, n);
+                    if (vec) {
+                        ptx::cp_async16(at + cell(tall, i) * 4, n > 0 ? M.p + e : M.p, n > 0 ? 16 : 0);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            ptx::cp_async4(at + cell(tall, i) * 4 + 4 * q, q < n ? M.p + e + q : M.p, q < n ? 4 : 0);
+                    }
+                }
+                ++fseq;
+                if (++fb == BLOCKS) {
+                    fb = 0;
+                    ++fu;
+                }
+            }
+            ptx::cp_async_commit();
+        };
+        fetch();
+        fetch();
+        uint32_t k = 0, seq = 0;
         for (int u = u0; u < u1; ++u, ++k) {
-            const int tile = u - A.apply0;
-            wait(&ofull[k & 1], (k >> 1) & 1u);
-            ptx::tc_fence_after();
+            if (u == end) {
+                ++mi;
+                pf = first_of(frec[mi & 1]);
+                end = frec[mi & 1].apply0 + frec[mi & 1].tiles;
+            }
+            const MuonMat& M = frec[mi & 1];
+            const int tile = u - M.apply0;
+            const bool tall = M.tall != 0, vec = aligned(M);
+            float* const pp = M.p;
+            __nv_bfloat16* const po = M.out;
+            const float decay = M.decay, scale = -M.step * M.hdr[1];
+            const uint64_t decay2 = ptx::f32x2(decay, decay), scale2 = ptx::f32x2(scale, scale);
 #pragma unroll 1
-            for (int b = 0; b < BLOCKS; ++b) {
+            for (int b = 0; b < BLOCKS; ++b, ++seq) {
+                float* const pl = places + (seq & 1) * (kApplyBlock / 4);
+                ptx::cp_async_wait<1>();
+                if (b == 0) {
+                    wait(&ofull[k & 1], (k >> 1) & 1u);
+                    ptx::tc_fence_after();
+                }
+                __syncwarp();
                 const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16) + (k & 1) * 256 + (b >> 1) * 128 + chalf +
                                        16 * (b & 1);
-                float o[16];
-                __syncwarp();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t hi[8], lo[8];
-                    ptx::tmem_ld8(t_row + 8 * h, hi);
-                    ptx::tmem_ld8(t_row + 64 + 8 * h, lo);
-                    ptx::tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[8 * h + i] = (__uint_as_float(hi[i]) + __uint_as_float(lo[i])) * A.osc;
-                }
+                uint32_t hi[16], lo[16];
+                ptx::tmem_ld16(t_row, hi);
+                ptx::tmem_ld16(t_row + 64, lo);
+                ptx::tmem_ld_wait();
                 if (b == BLOCKS - 1) {        // the accumulators have been read
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(&ofree[k & 1]);
                 }
-                float* const pp = A.p;
-                __nv_bfloat16* const po = A.out;
-                const float decay = A.decay, step = A.step;
-                const bool next = b + 1 < BLOCKS || u + 1 < u1;
-                auto request_next = [&]() {
-                    if (b + 1 < BLOCKS) {
-                        request(A, tile, b + 1);
-                    } else if (next) {
-                        if (u + 1 >= A.end) enter(A, ++mi);
-                        request(A, u + 1 - A.apply0, 0);
-                    }
+                auto update = [&](int i, float2 p) {
+                    const uint64_t o = ptx::f32x2_add(ptx::f32x2(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])),
+                                                      ptx::f32x2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])));
+                    return ptx::f32x2_get(ptx::f32x2_fma(scale2, o, ptx::f32x2_mul(ptx::f32x2(p.x, p.y), decay2)));
                 };
-                if (!aligned(A)) {
-                    // tall: lanes are consecutive elements of a column; not tall: each lane its row
-                    const int e0 = place(A, tile, (b >> 1) * 128 + quarter * 32 + lane, chalf + 16 * (b & 1));
-                    const int d = A.tall ? A.w : 1;
-                    // (the matrix can end inside the block)
-                    const int n = e0 < 0 ? 0 : A.tall ? (A.L * A.s - e0 + A.w - 1) / A.w : A.L - e0 % A.L;
-#pragma unroll
-                    for (int h = 0; h < 16; h += 8) {
-                        float pv[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) pv[i] = h + i < n ? pp[e0 + (h + i) * d] : 0.f;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (h + i < n) {
-                                const float v = fmaf(-step, o[h + i], pv[i] * decay);
-                                pp[e0 + (h + i) * d] = v;
-                                if (po) po[e0 + (h + i) * d] = __float2bfloat16_rn(v);
-                            }
-                    }
-                    request_next();
-                    continue;
-                }
-                const bool tall = A.tall != 0;
-                __syncwarp();
                 if (tall) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) stage[i * 32 + lane] = o[i];
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 v = update(i, make_float2(pl[i * 32 + lane], pl[(i + 1) * 32 + lane]));
+                        pl[i * 32 + lane] = v.x;
+                        pl[(i + 1) * 32 + lane] = v.y;
+                    }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<float4*>(stage + lane * 16 + ((i ^ (lane >> 1)) & 3) * 4) =
-                            make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                }
-                __syncwarp();
-                float4 v[4];
-                int e[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 8 * i + (lane >> 2);
-                    const float4 q = *reinterpret_cast<const float4*>(
-                        tall ? stage + (4 * i + (lane >> 3)) * 32 + (lane & 7) * 4
-                             : stage + r * 16 + (((lane & 3) ^ (r >> 1)) & 3) * 4);
-                    v[i].x = fmaf(-step, q.x, p[i].x * decay);
-                    v[i].y = fmaf(-step, q.y, p[i].y * decay);
-                    v[i].z = fmaf(-step, q.z, p[i].z * decay);
-                    v[i].w = fmaf(-step, q.w, p[i].w * decay);
-                    e[i] = at[i];
-                }
-                request_next();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (e[i] < 0) continue;
-                    *reinterpret_cast<float4*>(pp + e[i]) = v[i];
-                    if (po) {
-                        const __nv_bfloat162 va = __floats2bfloat162_rn(v[i].x, v[i].y), vb = __floats2bfloat162_rn(v[i].z, v[i].w);
-                        *reinterpret_cast<uint2*>(po + e[i]) = make_uint2(*reinterpret_cast<const uint32_t*>(&va),
-                                                                         *reinterpret_cast<const uint32_t*>(&vb));
+                    for (int i = 0; i < 4; ++i) {
+                        float4* const q = reinterpret_cast<float4*>(pl + lane * 16 + ((i ^ (lane >> 1)) & 3) * 4);
+                        const float4 p = *q;
+                        const float2 a = update(4 * i, make_float2(p.x, p.y)), c = update(4 * i + 2, make_float2(p.z, p.w));
+                        *q = make_float4(a.x, a.y, c.x, c.y);
                     }
                 }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    int n;
+                    const int e = quad(M, pf, tile, b, i, n);
+                    const float4 v = *reinterpret_cast<const float4*>(pl + cell(tall, i));
+                    if (vec) {
+                        if (n <= 0) continue;
+                        *reinterpret_cast<float4*>(pp + e) = v;
+                        if (po) {
+                            const __nv_bfloat162 va = __floats2bfloat162_rn(v.x, v.y), vb = __floats2bfloat162_rn(v.z, v.w);
+                            *reinterpret_cast<uint2*>(po + e) = make_uint2(*reinterpret_cast<const uint32_t*>(&va),
+                                                                          *reinterpret_cast<const uint32_t*>(&vb));
+                        }
+                    } else {
+                        const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (q < n) {
+                                pp[e + q] = x[q];
+                                if (po) po[e + q] = __float2bfloat16_rn(x[q]);
+                            }
+                    }
+                }
+                __syncwarp();      // (a lane's cells are read by itself last, but its row's by every lane)
+                fetch();
             }
         }
+        ptx::cp_async_wait<0>();
     } else {
-        ptx::reg_dec<kApplyRegsIssue>();
-    }
-    if (warp == kIssueWarp && lane == 0) {
         // ------------------------------------------------------------ products
+        // (the whole warp runs this, so that addresses stay in uniform registers; one lane issues)
+        const bool one = ptx::elect_one();
         uint32_t k = 0, nq = 0;      // tiles, and Q pieces (BIG) or whole Qs, so far
         int end = -1;                // first tile past the matrix
         bool tall = false;
@@ -1272,8 +1336,10 @@ muon_apply_kernel(const MuonMat* __restrict__ mats, int first, int last, int til
                 q = M.q;
                 if (!BIG) {
                     if (k > 0) wait(&ofull[(k - 1) & 1], ((k - 1) >> 1) & 1u);   // the products that read the last Q
-                    ptx::mbar_arrive_expect_tx(&qfull[0], kApplyQ);
-                    ptx::bulk_load(sq, q, kApplyQ, &qfull[0]);
+                    if (one) {
+                        ptx::mbar_arrive_expect_tx(&qfull[0], kApplyQ);
+                        ptx::bulk_load(sq, q, kApplyQ, &qfull[0]);
+                    }
                     wait(&qfull[0], nq & 1u);
                     ++nq;
                 }
@@ -1282,23 +1348,33 @@ muon_apply_kernel(const MuonMat* __restrict__ mats, int first, int last, int til
             const uint32_t vbase = sv0 + slot * 3 * kMuonPlane;
             const uint32_t d0 = tmem + (k & 1) * 256;
             // K step ks of the tile: its rows 16 ks ..
-            const uint64_t v0 = tall ? ptx::smem_desc_sw128(vbase, 16, 1024) : ptx::smem_desc_sw128(vbase, 8192, 1024);
-            auto vdesc = [&](int ks) {
-                return v0 + (tall ? (uint64_t)((ks >> 2) * 8192 + (ks & 3) * 32) / 16 : (uint64_t)ks * (2048 / 16));
+            const MuonDesc v0 = tall ? ptx::smem_desc_sw128(vbase, 16, 1024) : ptx::smem_desc_sw128(vbase, 8192, 1024);
+            auto v_at = [&](int ks) {
+                MuonDesc d = v0;
+                d.lo += tall ? (uint32_t)((ks >> 2) * 8192 + (ks & 3) * 32) / 16 : (uint32_t)ks * (2048 / 16);
+                return d;
             };
             wait(&vfull[slot], (k / PLACES) & 1u);
             if (k >= 2) wait(&ofree[k & 1], ((k >> 1) & 1u) ^ 1u);
             ptx::tc_fence_after();
             if constexpr (!BIG) {
-                const uint64_t q0 = ptx::smem_desc_sw128(sq0, 16, 1024);
-                for (int ks = 0; ks < ksteps; ++ks)
-                    muon_mma(d0, d0 + 64, q0 + (uint64_t)((ks >> 2) * 3 * kMuonPlane + (ks & 3) * 32) / 16, vdesc(ks),
-                             kMuonPlane / 16, PLANE / 16, idesc, ks == 0);
+                const MuonDesc q0 = ptx::smem_desc_sw128(sq0, 16, 1024);
+                if (one) {
+                muon_mma<true, false>(d0, d0 + 64, q0, v0, kMuonPlane / 16, PLANE / 16, idesc);
+#pragma unroll
+                for (int ks = 1; ks < 8; ++ks) {
+                    if (ks >= ksteps) break;
+                    MuonDesc d = q0;
+                    d.lo += (uint32_t)((ks >> 2) * 3 * kMuonPlane + (ks & 3) * 32) / 16;
+                    muon_mma<false, false>(d0, d0 + 64, d, v_at(ks), kMuonPlane / 16, PLANE / 16, idesc);
+                }
+                }
             } else {
                 const int kb = (ksteps + 3) / 4, pieces = 2 * kb;
                 auto fetch = [&](int c) {   // piece c: row half c / kb, column block c % kb
                     const uint32_t n = nq + c;
                     if (n >= 2) wait(&qfree[n & 1], ((n >> 1) & 1u) ^ 1u);
+                    if (!one) return;
                     ptx::mbar_arrive_expect_tx(&qfull[n & 1], 3 * kMuonPlane);
                     ptx::bulk_load(sq + (n & 1) * 3 * kMuonPlane, q + ((int64_t)(c / kb) * 4 + c % kb) * 3 * kMuonPlane,
                                    3 * kMuonPlane, &qfull[n & 1]);
@@ -1309,16 +1385,27 @@ muon_apply_kernel(const MuonMat* __restrict__ mats, int first, int last, int til
                     const uint32_t n = nq + c;
                     wait(&qfull[n & 1], (n >> 1) & 1u);
                     const int h = c / kb, b = c % kb;
-                    for (int ks = 0; ks < 4 && b * 4 + ks < ksteps; ++ks)
-                        muon_mma(d0 + h * 128, d0 + h * 128 + 64,
-                                 ptx::smem_desc_sw128(sq0 + (n & 1) * 3 * kMuonPlane + ks * 32, 16, 1024), vdesc(b * 4 + ks),
-                                 kMuonPlane / 16, PLANE / 16, idesc, b == 0 && ks == 0);
+                    const uint32_t dh = d0 + h * 128;
+                    const MuonDesc q0 = ptx::smem_desc_sw128(sq0 + (n & 1) * 3 * kMuonPlane, 16, 1024);
+                    if (one) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        if (b * 4 + ks >= ksteps) break;
+                        MuonDesc d = q0;
+                        d.lo += ks * 2;
+                        if (ks == 0 && b == 0) muon_mma<true, false>(dh, dh + 64, d, v_at(0), kMuonPlane / 16, PLANE / 16, idesc);
+                        else muon_mma<false, false>(dh, dh + 64, d, v_at(b * 4 + ks), kMuonPlane / 16, PLANE / 16, idesc);
+                    }
                     ptx::tc_commit(&qfree[n & 1]);
+                    }
                 }
                 nq += pieces;
             }
-            ptx::tc_commit(&vfree[slot]);
-            ptx::tc_commit(&ofull[k & 1]);
+            if (one) {
+                ptx::tc_commit(&vfree[slot]);
+                ptx::tc_commit(&ofull[k & 1]);
+            }
+            __syncwarp();
         }
     }
     __syncwarp();

@@ -130,6 +130,7 @@ def check(job, tol=O_TOL, eng=None):
     (8, 16, [3, 8, 13, 40]),             # ranks above both sizes: the short side is d_in or d_out
     (2056, 1032, [17, 128]),             # more than one Gram chunk, a ragged one
     (520, 264, [129, 200, 256]),         # the largest ranks
+    (16384, 8, [128, 128, 100, 17]),     # matrices of one tile between long ones, in the same block's run
 ])
 def test_matches_the_formula(dtype, d_in, d_out, ranks):
     check(Job(dtype, d_in, d_out, ranks, seed=len(ranks) + d_in))
