@@ -242,17 +242,13 @@ struct MuonTile {
             const int t0 = tile * kMuonTileL * M.J + col0;
 #pragma unroll
             for (int i = 0; i < NQ; ++i) quads(i, meta[i] + t0, meta[i] >= 0);
-        } else if (mode == kFlat) {
-            const int e0 = (tile * kMuonTileL + col0) * M.J * M.s + 4 * row, total = M.L * M.s;
+        } else if (mode == kFlat || mode == kPairs) {
+            // the step's TL w elements as they lie in memory (kPairs: for read_pairs)
+            const int n = TL * M.J * M.s, e0 = (tile * kMuonTileL + col0) * M.J * M.s, total = M.L * M.s - e0;
 #pragma unroll
-            for (int i = 0; i < NQ; ++i) quads(i, e0 + 4 * T * i, meta[i] >= 0 && e0 + 4 * T * i < total);
-        } else if (mode == kPairs) {
-            const int w = M.J * M.s, total = M.L * M.s, e0 = (tile * kMuonTileL + col0 + row) * w + x;
-#pragma unroll
-            for (int p = 0; p < 2 * NQ; ++p) {
-                const int e = e0 + p * kPairCols * w;
-                single(p >> 1, (p & 1) * 2, e, x < w && e < total);
-                single(p >> 1, (p & 1) * 2 + 1, e + 1, x + 1 < w && e + 1 < total);
+            for (int i = 0; i < NQ; ++i) {
+                const int f = 4 * ((int)threadIdx.x + i * T);
+                quads(i, e0 + f, f < n && f < total);
             }
         } else {
             const bool vec = ((M.tall ? M.s : M.L) & 3) == 0;      // whole quads or none
@@ -274,6 +270,21 @@ struct MuonTile {
         for (int i = 0; i < NQ; ++i) {
             set4(g[i], *reinterpret_cast<const float4*>(raw + i * T * 16));
             set4(m[i], *reinterpret_cast<const float4*>(raw + (NQ + i) * T * 16));
+        }
+    }
+    // kPairs: this thread's pairs out of a step that the block's threads have fetched to `raw` (its first cell)
+    __device__ __forceinline__ void read_pairs(const MuonMat& M, const uint8_t* raw, float (&g)[NQ][4], float (&m)[NQ][4]) const {
+        const int w = M.J * M.s;
+        const float* const pg = reinterpret_cast<const float*>(raw) + row * w + x;
+        const float* const pm = pg + NQ * T * 4;
+        const bool a = x < w, b = x + 1 < w;
+#pragma unroll
+        for (int p = 0; p < 2 * NQ; ++p) {
+            const int e = p * kPairCols * w;
+            g[p >> 1][(p & 1) * 2] = a ? pg[e] : 0.f;
+            g[p >> 1][(p & 1) * 2 + 1] = b ? pg[e + 1] : 0.f;
+            m[p >> 1][(p & 1) * 2] = a ? pm[e] : 0.f;
+            m[p >> 1][(p & 1) * 2 + 1] = b ? pm[e + 1] : 0.f;
         }
     }
     // stores v to where load() took it from in `dst`
@@ -441,8 +452,8 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
         ptx::cp_async_commit();
         if (t0 + 1 < t1) T.fetch(M, t0 + 1, 0, raw_cells + kGramRaw);
         ptx::cp_async_commit();
-        const float mu = M.mu;
-        const bool nesterov = M.nesterov != 0;
+        const uint64_t mu2 = ptx::f32x2(M.mu, M.mu);
+        const bool nesterov = M.nesterov != 0, pairs = T.mode == Tile::kPairs;
         uint32_t count = 0;     // tiles handed over: the k-th went to place k & 1
         int since = 0;          // tiles in the accumulators
         float scale = 0.f;      // 2^-unit
@@ -473,6 +484,12 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
                 ptx::tmem_ld16(t_row + c0, hi);
                 ptx::tmem_ld16(t_row + 128 + c0, lo);
                 ptx::tmem_ld_wait();
+                // a diagonal block is in several pairs: the pair with the next group writes it (the last group's, the
+                // pair with the one before)
+                const int gr = r < 64 ? ga : gb, gc = c0 < 64 ? ga : gb, rr = gr * 64 + (r & 63);
+                const bool own = (gr != gc || (gr == ga ? gb == ga + 1 : ga == ng - 2)) && rr < M.s;
+                double* const o = out + (gc * 64 + (c0 & 63)) * M.s + rr;      // lanes on consecutive addresses
+                const int cols = min(16, M.s - (gc * 64 + (c0 & 63)));
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     const int c = c0 + k;
@@ -480,16 +497,8 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
                     const double v = muon_to_double(__uint_as_float(hi[k]), k2) + muon_to_double(__uint_as_float(lo[k]), k2);
                     if (M.J > 1) {
                         if (j < M.J && c >= j * M.s) stack[(c - j * M.s) * 128 + r] = v;
-                    } else {
-                        const int gr = r < 64 ? ga : gb, gc = c < 64 ? ga : gb;
-                        const int rr = gr * 64 + (r & 63), cc = gc * 64 + (c & 63);
-                        // a diagonal block is in several pairs: the pair with the next group writes it (the last
-                        // group's, the pair with the one before)
-                        const bool own = gr != gc || (gr == ga ? gb == ga + 1 : ga == ng - 2);
-                        if (own && rr < M.s && cc < M.s) {
-                            double* o = out + cc * M.s + rr;      // lanes on consecutive addresses
-                            *o = stored ? *o + v : v;
-                        }
+                    } else if (own && k < cols) {
+                        o[k * M.s] = stored ? o[k * M.s] + v : v;
                     }
                 }
             }
@@ -529,39 +538,45 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
                 float g[Tile::NQ][4], m[Tile::NQ][4];
                 uint8_t* const cells = raw_cells + ((t - t0) & 1) * kGramRaw;
                 ptx::cp_async_wait<1>();
-                Tile::read(cells, g, m);
+                if (pairs) {
+                    sync();                             // other threads' copies are read
+                    T.read_pairs(M, cells - tid * 16, g, m);
+                } else {
+                    Tile::read(cells, g, m);
+                }
 #pragma unroll
                 for (int i = 0; i < Tile::NQ; ++i)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float mn = fmaf(mu, m[i][k], g[i][k]);
-                        u[i][k] = nesterov ? fmaf(mu, mn, g[i][k]) : mn;
+                    for (int k = 0; k < 4; k += 2) {
+                        const uint64_t gg = ptx::f32x2(g[i][k], g[i][k + 1]);
+                        const uint64_t a = ptx::f32x2_fma(mu2, ptx::f32x2(m[i][k], m[i][k + 1]), gg);
+                        const float2 c = ptx::f32x2_get(nesterov ? ptx::f32x2_fma(mu2, a, gg) : a);
+                        u[i][k] = c.x;
+                        u[i][k + 1] = c.y;
                     }
-                if (t + 2 < t1) T.fetch(M, t + 2, 0, cells);
-                ptx::cp_async_commit();
+                if (!pairs) {
+                    if (t + 2 < t1) T.fetch(M, t + 2, 0, cells);
+                    ptx::cp_async_commit();
+                }
             }
             float big = 0.f;
-            bool over = scale == 0.f;
 #pragma unroll
             for (int i = 0; i < Tile::NQ; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float a = fabsf(u[i][k]);
-                    over = over || !(a * scale <= 128.f);      // also a NaN
-                    big = fmaxf(big, a);
-                }
+                for (int k = 0; k < 4; ++k) big = ptx::max_nan(big, fabsf(u[i][k]));
             item_max = fmaxf(item_max, big);
+            bool over = scale == 0.f || !(big * scale <= 128.f);      // also a NaN
             // (the first tile has no scale yet; a first tile of zeros leaves it to the next)
             over = ptx::named_bar_or(1, kGramLoad, over);
+            if (pairs) {                                // every thread has read the cells
+                if (t + 2 < t1) T.fetch(M, t + 2, 0, raw_cells + ((t - t0) & 1) * kGramRaw);
+                ptx::cp_async_commit();
+            }
             if (over || since == kGramExactTiles) {
                 if (since > 0) drain();
                 if (over) {
                     float w = big;
-                    bool nan = false;
-#pragma unroll
-                    for (int i = 0; i < Tile::NQ; ++i)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) nan = nan || !(u[i][k] * 0.f == 0.f);
+                    const bool nan = !(big * 0.f == 0.f);      // or an infinity
                     for (int o = 16; o > 0; o >>= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, o));
                     if (lane == 0) red[warp] = w;
                     bad = ptx::named_bar_or(1, kGramLoad, nan) || bad;
@@ -605,7 +620,9 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
             for (int k = 0; k < kGramLoad / 32; ++k) w = fmaxf(w, red[k]);
             M.hdr[2 + item] = w;
         }
-    } else if (lane == 0) {
+    } else {
+        // (the whole warp runs this, so that addresses stay in uniform registers; one lane issues)
+        const bool one = ptx::elect_one();
         const bool tall = M.tall != 0;
         const uint32_t idesc = ptx::idesc_f16_f32(128, 128, tall, tall);
         for (uint32_t k = 0;; ++k) {
@@ -616,15 +633,19 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
             ptx::tc_fence_after();
             const uint32_t base = s0 + place * kGramStage;
             const uint32_t kstep = tall ? 2048 / 16 : 32 / 16;
-            MuonDesc d = tall ? ptx::smem_desc_sw128(base, 8192, 1024) : ptx::smem_desc_sw128(base, 16, 1024);
-            if (todo == kStart) muon_mma<true, true>(tmem, tmem + 128, d, d, kMuonPlane / 16, kMuonPlane / 16, idesc);
-            else muon_mma<false, true>(tmem, tmem + 128, d, d, kMuonPlane / 16, kMuonPlane / 16, idesc);
+            const MuonDesc d0 = tall ? ptx::smem_desc_sw128(base, 8192, 1024) : ptx::smem_desc_sw128(base, 16, 1024);
+            if (one) {
+                MuonDesc d = d0;
+                if (todo == kStart) muon_mma<true, true>(tmem, tmem + 128, d, d, kMuonPlane / 16, kMuonPlane / 16, idesc);
+                else muon_mma<false, true>(tmem, tmem + 128, d, d, kMuonPlane / 16, kMuonPlane / 16, idesc);
 #pragma unroll
-            for (int q = 1; q < kMuonTileL / 16; ++q) {
-                d.lo += kstep;
-                muon_mma<false, true>(tmem, tmem + 128, d, d, kMuonPlane / 16, kMuonPlane / 16, idesc);
+                for (int q = 1; q < kMuonTileL / 16; ++q) {
+                    d.lo += kstep;
+                    muon_mma<false, true>(tmem, tmem + 128, d, d, kMuonPlane / 16, kMuonPlane / 16, idesc);
+                }
+                ptx::tc_commit(&done[place]);
             }
-            ptx::tc_commit(&done[place]);
+            __syncwarp();
         }
     }
     __syncwarp();
@@ -1186,6 +1207,14 @@ muon_apply_kernel(const MuonMat* __restrict__ mats, int first, int last, int til
             return e;
         };
         auto aligned = [](const MuonMat& M) { return ((M.tall ? M.J * M.s : M.L) & 3) == 0; };
+        // tall and not aligned: a lane keeps its row, whose elements lie w apart: the first, and how many exist
+        auto column = [&](const MuonMat& M, int tile, int b, int& n) {
+            const int w = M.J * M.s, r = (b >> 1) * 128 + quarter * 32 + lane;
+            const int e = (tile * kMuonTileL + chalf + 16 * (b & 1)) * w + r;
+            n = r < w ? 16 : 0;
+            if (n && tile + 1 >= M.tiles) n = max(0, min(16, (M.L * M.s - e + w - 1) / w));
+            return e;
+        };
         auto cell = [&](bool tall, int i) {
             const int r = 8 * i + (lane >> 2);
             return tall ? (4 * i + (lane >> 3)) * 32 + (lane & 7) * 4 : r * 16 + (((lane & 3) ^ (r >> 1)) & 3) * 4;
@@ -1209,6 +1238,13 @@ muon_apply_kernel(const MuonMat* __restrict__ mats, int first, int last, int til
                 const MuonMat& M = frec[fmi & 1];
                 const uint32_t at = ptx::smem_u32(places) + (fseq & 1) * kApplyBlock;
                 const bool vec = aligned(M), tall = M.tall != 0;
+                if (tall && !vec) {
+                    int n;
+                    const int e = column(M, fu - M.apply0, fb, n), w = M.J * M.s;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        ptx::cp_async4(at + (i * 32 + lane) * 4, i < n ? M.p + e + i * w : M.p, i < n ? 4 : 0);
+                } else
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     int n;
@@ -1270,6 +1306,26 @@ muon_apply_kernel(const MuonMat* __restrict__ mats, int first, int last, int til
                                                       ptx::f32x2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])));
                     return ptx::f32x2_get(ptx::f32x2_fma(scale2, o, ptx::f32x2_mul(ptx::f32x2(p.x, p.y), decay2)));
                 };
+                if (tall && !vec) {
+                    int n;
+                    const int e = column(M, tile, b, n), w = M.J * M.s;
+                    float* const q = pp + e;
+                    __nv_bfloat16* const qo = po + e;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 v = update(i, make_float2(pl[i * 32 + lane], pl[(i + 1) * 32 + lane]));
+                        if (i < n) {
+                            q[i * w] = v.x;
+                            if (po) qo[i * w] = __float2bfloat16_rn(v.x);
+                        }
+                        if (i + 1 < n) {
+                            q[(i + 1) * w] = v.y;
+                            if (po) qo[(i + 1) * w] = __float2bfloat16_rn(v.y);
+                        }
+                    }
+                    fetch();       // (into this lane's own cells)
+                    continue;
+                }
                 if (tall) {
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
