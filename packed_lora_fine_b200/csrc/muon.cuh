@@ -40,8 +40,6 @@ namespace plora {
 
 constexpr int kMuonTileL = 64;        // columns l' of a tile
 constexpr int kMuonPlane = 128 * kMuonTileL * 2;   // bytes of one fp16 part of a tile (16 KB)
-constexpr int kMuonNsTile = 32;       // product tile of the iteration
-constexpr int kMuonCluster = 8;       // blocks per matrix in the iteration
 constexpr int kMuonBigS = 128;        // above: two 128-row halves per tile in the apply pass
 
 // One matrix of the step.  Element (c, l), c on the short side: c * L + l if !tall, l * s + c if tall.
@@ -51,9 +49,9 @@ struct MuonMat {
     float* p;
     __nv_bfloat16* out;   // the layer's bf16 copy, or nullptr when p is the parameter
     double* part;         // [nchunks][s][s] Gram partials
-    double* ns;           // five [sp][sp] matrices of the iteration, sp = s rounded up to 8 (s > 64)
+    double* ns;           // G, P and Q, [sp][sp], sp = s rounded up to 8 (s > 128)
     uint8_t* q;           // Q's fp16 parts as the apply pass stages them (muon_q_at)
-    float* hdr;           // x scale, output scale, max|u| of each Gram item, max|Q| of each block
+    float* hdr;           // x scale, output scale, max|u| of each Gram item
     int32_t s, L;
     int32_t tall, nesterov;
     int32_t steps;
@@ -656,11 +654,27 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
 }
 
 // ----------------------------------------------------------------------------------------- iteration
-constexpr int kNsK = 64;                               // K extent of one stage
-constexpr int kNsPitch = kNsK + 4;                     // doubles; rows shift by 4 so that fragment loads spread
-constexpr int kNsStages = 3;
-constexpr int kNsStageD = 2 * kMuonNsTile * kNsPitch;  // doubles of one stage: the A rows, then the B rows
-constexpr int kMuonNsSmem = (kNsStages * kNsStageD + 4 * 32 * 8) * 8;
+// Three forms, by s, all on the fp64 tensor cores (64 multiply-adds per clock and SM):
+//   s <= 64    one block, G, P and Q in shared memory, the lower halves of the products
+//   s <= 128   a cluster of four blocks, each with 32 rows of G and Q and a copy of the whole matrix that is the
+//              right-hand operand: first G (for P = a I + b G + c G^2), then P.  With P at hand a block's rows of
+//              Q P, of R = G P and of the new G = R P need nothing of the others', so a step takes two exchanges,
+//              each block copying its rows into every block's matrix
+//   s <= 256   a cluster of eight blocks with 32 rows each.  The matrices are in L2, where they come from in
+//              stages; a block computes the blocks of its rows on and after the diagonal, half of them, cyclically,
+//              and writes them to both places.
+// (Products of symmetric matrices that commute are symmetric: B's rows serve as its columns.)
+constexpr int kNsRows = 32;                            // rows of a cluster's block
+constexpr int kNsPitch = 64 + 4;                       // doubles; rows shift by 4 so that fragment loads spread
+constexpr int kNsSmallS = 64;
+constexpr int kNsMidS = 128, kNsMidPitch = kNsMidS + 4, kNsMidCluster = kNsMidS / kNsRows;
+constexpr int kNsBigPitch = 256 + 4, kNsBigCluster = 256 / kNsRows;
+constexpr int kNsK = 32, kNsStages = 4, kNsStage = kNsRows * (kNsK + 4);   // doubles of one stage of the streamed operand
+constexpr int kNsSmallSmem = 3 * kNsSmallS * kNsPitch * 8;
+constexpr int kNsMidSmem = (kNsMidS + 2 * kNsRows) * kNsMidPitch * 8;
+constexpr int kNsBigSmem = (kNsRows * kNsBigPitch + kNsStages * kNsStage) * 8;
+static_assert(kNsSmallSmem <= kNsMidSmem && kNsMidSmem + 2048 <= 232448, "shared memory per CTA");
+static_assert(2 * (kNsBigSmem + 2048) <= 232448, "two CTAs per SM");
 
 __device__ __forceinline__ void dmma_16x8x8(double (&d)[4], const double (&a)[4], const double (&b)[2]) {
     asm volatile(
@@ -668,120 +682,47 @@ __device__ __forceinline__ void dmma_16x8x8(double (&d)[4], const double (&a)[4]
         : "+d"(d[0]), "+d"(d[1]), "+d"(d[2]), "+d"(d[3])
         : "d"(a[0]), "d"(a[1]), "d"(a[2]), "d"(a[3]), "d"(b[0]), "d"(b[1]));
 }
-
-// One product of the iteration: C = A B for symmetric sp x sp matrices that commute, so that C is symmetric
-// (only elements with c <= r are computed) and B's rows serve as its columns.
-struct NsProduct {
-    const double* A;
-    const double* B;
-    int what;          // passed on to `out`
-};
-
-// Up to two products over a cluster: the 32 x 32 tiles of their lower halves dealt over its blocks, each with
-// its K in stages of 64 that run ahead across tiles.  out(what, r, c, v) takes each element.
-// Eight warps: 2 x 2 blocks of 16 x 16, two interleaved halves of each stage's K, joined in a fixed order.
-template <typename F>
-__device__ __forceinline__ void ns_products(const NsProduct& p0, const NsProduct& p1, int n, int sp, int rank, double* sm,
-                                            F&& out) {
-    constexpr int T = kMuonNsTile;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int wr = (warp & 1) * 16, wc = ((warp >> 1) & 1) * 16, kh = warp >> 2;
-    const int nt = (sp + T - 1) / T, each = nt * (nt + 1) / 2, tiles = n * each, nk = (sp + kNsK - 1) / kNsK;
-    // a cursor over this block's (tile, K stage) steps
-    struct Cursor {
-        int t, ti, tj, kc, st;
-        bool second;
-    };
-    auto place = [&](Cursor& c) {
-        int t = c.t;
-        c.second = t >= each;
-        if (c.second) t -= each;
-        c.ti = 0;
-        while (t > c.ti) { t -= c.ti + 1; ++c.ti; }
-        c.tj = t;
-        c.kc = 0;
-    };
-    auto next = [&](Cursor& c) {
-        if (++c.st == kNsStages) c.st = 0;
-        if (++c.kc == nk) {
-            c.t += kMuonCluster;
-            place(c);
+// acc (16 R x 8 N) += the 16 R rows at `a` times the 8 N rows at `b`, over k8 steps of eight.
+template <int R, int N>
+__device__ __forceinline__ void dmma_block(double (&acc)[R][N][4], const double* a, int ap, const double* b, int bp, int k8) {
+    const int lane = threadIdx.x & 31;
+    const double* as = a + (lane >> 2) * ap + (lane & 3);
+    const double* bs = b + (lane >> 2) * bp + (lane & 3);
+#pragma unroll 4
+    for (int k = 0; k < k8; ++k, as += 8, bs += 8) {
+        double x[R][4], y[N][2];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const double* p = as + 16 * i * ap;
+            x[i][0] = p[0];
+            x[i][1] = p[8 * ap];
+            x[i][2] = p[4];
+            x[i][3] = p[8 * ap + 4];
         }
-    };
-    Cursor fc{rank, 0, 0, 0, 0, false};
-    place(fc);
-    Cursor cc = fc;
-    // this thread's pieces of a stage: 16 bytes at column fcol of rows frow + 8 i of A's and of B's tile
-    const int frow = tid >> 5, fcol = (tid & 31) * 2;
-    auto fetch = [&]() {
-        if (fc.t < tiles) {
-            const NsProduct& p = fc.second ? p1 : p0;
-            const int k0 = fc.kc * kNsK + fcol, ra = fc.ti * T + frow, rb = fc.tj * T + frow;
-            const bool kin = k0 < sp;
-            const double* a = p.A + (kin ? ra * sp + k0 : 0);
-            const double* b = p.B + (kin ? rb * sp + k0 : 0);
-            const uint32_t dst = ptx::smem_u32(sm + fc.st * kNsStageD + frow * kNsPitch + fcol);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool ia = kin && ra + 8 * i < sp, ib = kin && rb + 8 * i < sp;
-                ptx::cp_async16(dst + 8 * i * kNsPitch * 8, ia ? a + 8 * i * sp : p.A, ia ? 16 : 0);
-                ptx::cp_async16(dst + (T + 8 * i) * kNsPitch * 8, ib ? b + 8 * i * sp : p.B, ib ? 16 : 0);
-            }
-            next(fc);
+        for (int j = 0; j < N; ++j) {
+            y[j][0] = bs[8 * j * bp];
+            y[j][1] = bs[8 * j * bp + 4];
         }
-        ptx::cp_async_commit();
-    };
-    double acc[2][4] = {};
-    for (int k = 0; k < kNsStages - 1; ++k) fetch();
-    while (cc.t < tiles) {
-        ptx::cp_async_wait<kNsStages - 2>();
-        __syncthreads();                      // the stage is there, and every warp has left the one fetched next
-        fetch();
-        const int kn = sp - cc.kc * kNsK;     // a multiple of 8
-        const double* as = sm + cc.st * kNsStageD + (wr + (lane >> 2)) * kNsPitch + (lane & 3);
-        const double* bs = sm + cc.st * kNsStageD + (T + wc + (lane >> 2)) * kNsPitch + (lane & 3);
 #pragma unroll
-        for (int q = 0; q < kNsK / 16; ++q) {
-            const int kk = q * 16 + kh * 8;
-            if (kk < kn) {
-                const double a[4] = {as[kk], as[kk + 8 * kNsPitch], as[kk + 4], as[kk + 8 * kNsPitch + 4]};
-                const double b0[2] = {bs[kk], bs[kk + 4]};
-                const double b1[2] = {bs[kk + 8 * kNsPitch], bs[kk + 8 * kNsPitch + 4]};
-                dmma_16x8x8(acc[0], a, b0);
-                dmma_16x8x8(acc[1], a, b1);
-            }
-        }
-        if (cc.kc == nk - 1) {   // the tile is complete
-            double* red = sm + kNsStages * kNsStageD + ((warp & 3) * 32 + lane) * 8;
-            if (kh) {
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) red[4 * j + i] = acc[j][i];
-            }
-            __syncthreads();
-            if (!kh) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = cc.ti * T + wr + (lane >> 2) + (i >> 1) * 8;
-                        const int c = cc.tj * T + wc + j * 8 + (lane & 3) * 2 + (i & 1);
-                        if (r < sp && c <= r) out(cc.second ? p1.what : p0.what, r, c, acc[j][i] + red[4 * j + i]);
-                    }
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[j][i] = 0.0;
-        }
-        next(cc);
+            for (int j = 0; j < N; ++j) dmma_16x8x8(acc[i][j], x[i], y[j]);
     }
-    ptx::cp_async_wait<0>();
-    __syncthreads();
+}
+// That block's elements of this lane, two neighbours at a time: f(row, column, value, its right neighbour).
+template <int R, int N, typename F> __device__ __forceinline__ void dmma_each(const double (&acc)[R][N][4], F&& f) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                f(16 * i + (lane >> 2) + 8 * h, 8 * j + (lane & 3) * 2, acc[i][j][2 * h], acc[i][j][2 * h + 1]);
 }
 
-// The same for s <= 64 on one block with its matrices in shared memory (pitch kNsPitch): the 10 blocks of
+// A product for s <= 64 on one block with its matrices in shared memory (pitch kNsPitch): the 10 blocks of
 // 16 x 16 of the lower half over the eight warps, their results kept in registers until every warp has
 // read its operands, so that C may be A or B.
 template <typename F>
@@ -837,98 +778,254 @@ __host__ __device__ __forceinline__ int64_t muon_q_at(int kblocks, int row, int 
     return block * kMuonPlane + r * 128 + (((k8 & 7) ^ (r & 7)) << 4);
 }
 
-constexpr int kNsSmallS = 64;
-static_assert(3 * kNsSmallS * kNsPitch * 8 <= kMuonNsSmem, "G, P and Q of a small matrix in shared memory");
+// Where the Gram matrix stands, sp x sp with zeros past s, for the iteration to scale.
+__device__ __forceinline__ double* muon_gram_at(const MuonMat& M) {
+    const int64_t sp = (M.s + 7) & ~7;
+    return M.ns + (M.s > kNsMidS ? 4 * sp * sp : 0);
+}
+// The sum of the Gram partials (their halves [c][r], r >= c, in the chunks' order), to both halves.  kSumBlocks
+// blocks per matrix, a warp per row at a time: 16 loads of 8 bytes in flight per thread.  (Summed by the iteration's
+// few blocks instead, 64 partials of 128 x 128 took 200 us of its 316.)
+constexpr int kSumBlocks = 32;
+__global__ void __launch_bounds__(256) muon_sum_kernel(const MuonMat* __restrict__ mats) {
+    const MuonMat& M = mats[blockIdx.x / kSumBlocks];
+    const int s = M.s, sp = (s + 7) & ~7, s2 = s * s, chunks = M.nchunks, lane = threadIdx.x & 31;
+    double* const G = muon_gram_at(M);
+    const double* const part = M.part;
+    for (int c = (blockIdx.x % kSumBlocks) * 8 + (threadIdx.x >> 5); c < sp; c += kSumBlocks * 8)
+        for (int r0 = (c & ~31) + lane; r0 < sp; r0 += 128) {
+            double g[4] = {};
+            bool ok[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ok[q] = c < s && r0 + 32 * q >= c && r0 + 32 * q < s;
+            const double* p = part + (int64_t)c * s + r0;
+            int ch = 0;
+            for (; ch + 4 <= chunks; ch += 4, p += 4 * (int64_t)s2) {
+                double v[4][4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[k][q] = ok[q] ? p[k * (int64_t)s2 + 32 * q] : 0.0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) g[q] += v[k][q];
+            }
+            for (; ch < chunks; ++ch, p += s2)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) g[q] += ok[q] ? p[32 * q] : 0.0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int r = r0 + 32 * q;
+                if (r < c || r >= sp) continue;
+                G[c * sp + r] = g[q];
+                G[r * sp + c] = g[q];
+            }
+        }
+}
 
-// The iteration on the matrices' Gram matrices in fp64 on the fp64 tensor cores.  s > 64: a cluster of eight
-// blocks per matrix, the matrices in L2, one cluster barrier after each round of products; s <= 64: one
-// block, the matrices in shared memory.  order: the matrices, those with s > 64 (n_big of them) first.
-// Then Q's three fp16 parts for the apply pass (block-diagonal over the stacked blocks) and the scales.
-__global__ void __cluster_dims__(kMuonCluster, 1, 1) __launch_bounds__(256)
-muon_ns_kernel(const MuonMat* __restrict__ mats, const int32_t* __restrict__ order, int n_big, int n) {
+// The iteration on the matrices' Gram matrices, then Q's three fp16 parts for the apply pass (block-diagonal over
+// the stacked blocks) and the scales.  order: n matrices, BIG: those with s > 128, a cluster of eight each; else
+// n_mid of s > 64, a cluster of four each, and then those that take a block each.
+template <bool BIG>
+__global__ void __launch_bounds__(256)
+muon_ns_kernel(const MuonMat* __restrict__ mats, const int32_t* __restrict__ order, int n_mid, int n, int* err_flag,
+               uint64_t timeout_ns) {
+    constexpr int CLUSTER = BIG ? kNsBigCluster : kNsMidCluster;
     extern __shared__ __align__(16) double sm[];
     __shared__ double redd[8];
-    __shared__ float redf[8];
+    __shared__ float redf[8], qmaxes[CLUSTER];
     __shared__ MuonMat record;
-    const bool small = blockIdx.x >= (unsigned)n_big * kMuonCluster;
-    const int which = small ? n_big + (int)blockIdx.x - n_big * kMuonCluster : (int)blockIdx.x / kMuonCluster;
+    __shared__ __align__(8) uint64_t arrived;
+    __shared__ int abort_flag;
+    const bool small = !BIG && blockIdx.x >= (unsigned)n_mid * CLUSTER;
+    const int which = small ? n_mid + (int)blockIdx.x - n_mid * CLUSTER : (int)blockIdx.x / CLUSTER;
     if (which >= n) return;      // the last cluster's spare blocks (their cluster holds small matrices only)
     muon_fetch(&record, mats + order[which]);
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(&arrived, 1);
+        abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
     __syncthreads();
     const MuonMat& M = record;
-    const int rank = small ? 0 : (int)ptx::cluster_ctarank(), ranks = small ? 1 : kMuonCluster;
-    const int tid = threadIdx.x, s = M.s, sp = (s + 7) & ~7;
-    const int s2 = s * s, pitch = small ? kNsPitch : sp, rows = small ? ((sp + 15) & ~15) : sp;
-    double* G = small ? sm : M.ns;
-    double* P = G + (small ? kNsSmallS * kNsPitch : sp * sp);
-    double* Q = P + (small ? kNsSmallS * kNsPitch : sp * sp);
-    double* R = Q + (small ? 0 : sp * sp);      // (the small products need no fourth matrix)
-    // |u|_F^2, the trace of G, and max |u|: by every block in the same order
-    double tr = 0.0;
-    for (int e = tid; e < s * M.nchunks; e += 256) {
-        const int d = e % s, ch = e / s;
-        tr += M.part[(int64_t)ch * s2 + d * (s + 1)];
-    }
-    float big = 0.f;
-    for (int e = tid; e < M.nchunks * M.npairs; e += 256) big = fmaxf(big, M.hdr[2 + e]);
-    for (int o = 16; o > 0; o >>= 1) {
-        tr += __shfl_xor_sync(0xffffffffu, tr, o);
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-    }
-    if ((tid & 31) == 0) { redd[tid >> 5] = tr; redf[tid >> 5] = big; }
-    __syncthreads();
-    tr = 0.0;
-    big = 0.f;
-    for (int w = 0; w < 8; ++w) { tr += redd[w]; big = fmaxf(big, redf[w]); }
-    const double inv = 1.0 / (sqrt(tr) + (double)M.eps);
-    // G, from the halves of the partials: four elements per thread and four chunks in flight
-    const int step = 256 * ranks, cells = rows * pitch;
-    for (int e0 = rank * 256 + tid; e0 < cells; e0 += 4 * step) {
-        double g[4] = {};
-        int at[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int e = e0 + q * step, r = e / pitch, c = e - r * pitch;
-            at[q] = e < cells && r < s && c < s ? min(r, c) * s + max(r, c) : -1;
-        }
-        int ch = 0;
-        for (; ch + 4 <= M.nchunks; ch += 4) {
-            double v[4][4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[k][q] = at[q] >= 0 ? M.part[(int64_t)(ch + k) * s2 + at[q]] : 0.0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) g[q] += v[k][q];
-        }
-        for (; ch < M.nchunks; ++ch)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) g[q] += at[q] >= 0 ? M.part[(int64_t)ch * s2 + at[q]] : 0.0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int e = e0 + q * step;
-            if (e >= cells) continue;
-            G[e] = (g[q] * inv) * inv;
-            if (small) P[e] = Q[e] = 0.0;
-        }
-    }
+    const int rank = small ? 0 : (int)ptx::cluster_ctarank();
+    const int tid = threadIdx.x, warp = tid >> 5, s = M.s, sp = (s + 7) & ~7, k8 = sp / 8;
+    // this block's rows of G and Q (from row r0 of the matrix on), and its own copies' pitch
+    const int nr = small ? s : kNsRows, r0 = rank * kNsRows;
+    const int pitch = BIG ? kNsBigPitch : small ? kNsPitch : kNsMidPitch;
+    // small: G, P, Q; mid: the matrix, then the block's rows of G and Q; big: the rows of the left operand, stages
+    double* const G = BIG || small ? sm : sm + kNsMidS * kNsMidPitch;
+    double* const Q = BIG ? sm : small ? G + 2 * kNsSmallS * kNsPitch : G + kNsRows * kNsMidPitch;
     auto sync = [&] {
         if (small) __syncthreads();
         else ptx::cluster_sync();
     };
+    // |u|_F^2, the trace of G, and max |u|: by every block in the same order
+    const double* const raw = muon_gram_at(M);
+    double tr = 0.0;
+    for (int e = tid; e < s; e += 256) tr += raw[e * (sp + 1)];
+    float umax = 0.f;
+    for (int e = tid; e < M.nchunks * M.npairs; e += 256) umax = fmaxf(umax, M.hdr[2 + e]);
+    auto block_sum = [&](double v) {
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        __syncthreads();
+        if ((tid & 31) == 0) redd[warp] = v;
+        __syncthreads();
+        v = 0.0;
+        for (int w = 0; w < 8; ++w) v += redd[w];
+        return v;
+    };
+    auto block_max = [&](float v) {
+        for (int o = 16; o > 0; o >>= 1) v = ptx::max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+        __syncthreads();
+        if ((tid & 31) == 0) redf[warp] = v;
+        __syncthreads();
+        v = 0.f;
+        for (int w = 0; w < 8; ++w) v = ptx::max_nan(v, redf[w]);
+        return v;
+    };
+    tr = block_sum(tr);
+    umax = block_max(umax);
+    const double inv = 1.0 / (sqrt(tr) + (double)M.eps);
+    // zeros past s, and the scaled G: its own rows, and as the first right-hand operand
+    {
+        const int cells = BIG ? kNsRows * kNsBigPitch : (small ? kNsSmallSmem : kNsMidSmem) / 8;
+        for (int e = tid; e < cells / 2; e += 256) reinterpret_cast<double2*>(sm)[e] = make_double2(0.0, 0.0);
+        __syncthreads();
+        const int h = sp / 2, rows = BIG ? min(kNsRows, sp - r0) : sp;
+#pragma unroll 4
+        for (int e = tid; e < rows * h; e += 256) {
+            const int r = e / h, c2 = e - r * h;
+            double2 v = reinterpret_cast<const double2*>(raw)[(BIG ? r0 + r : r) * h + c2];
+            v.x = (v.x * inv) * inv;
+            v.y = (v.y * inv) * inv;
+            *reinterpret_cast<double2*>(sm + r * pitch + 2 * c2) = v;
+            if (BIG) reinterpret_cast<double2*>(M.ns)[(r0 + r) * h + c2] = v;
+            if (!BIG && !small && r >= r0 && r < r0 + kNsRows) *reinterpret_cast<double2*>(G + (r - r0) * pitch + 2 * c2) = v;
+        }
+    }
     sync();
     const double a = M.a, b = M.b, c = M.c;
-    auto both = [&](double* C, int i, int j, double v) {
-        C[i * pitch + j] = v;
-        C[j * pitch + i] = v;
-    };
-    if (small) {
+    if constexpr (BIG) {
+        double* gG = M.ns;
+        double *gP = gG + sp * sp, *gQ = gP + sp * sp, *gR = gQ + sp * sp, *gS = gR + sp * sp;
+        double* const stages = sm + kNsRows * kNsBigPitch;
+        const int n = (s + kNsRows - 1) / kNsRows;        // blocks of 32 rows, and of 32 columns
+        const bool work = rank < n;
+        // rows of `X` for the left operand
+        auto rows_of = [&](const double* X) {
+            __syncthreads();
+            for (int e = tid; e < kNsRows * (sp / 2); e += 256) {
+                const int r = e / (sp / 2), c = (e - r * (sp / 2)) * 2;
+                const bool ok = r0 + r < sp;
+                ptx::cp_async16(ptx::smem_u32(G + r * kNsBigPitch + c), ok ? X + (r0 + r) * sp + c : X, ok ? 16 : 0);
+            }
+            ptx::cp_async_commit();               // (product waits for it with its first stage)
+        };
+        // C = f(those rows times X): the blocks (rank, rank + d mod n), 32 x 32 each, a warp's share 16 x 8
+        const int wr = (warp & 1) * 16, wc = (warp >> 1) * 8;
+        auto product = [&](const double* X, double* C, auto&& f) {
+            const int nk = (sp + kNsK - 1) / kNsK, steps = (n / 2 + 1) * nk;
+            const int fr = tid >> 4, fc = (tid & 15) * 2;      // this thread's pieces of a stage: rows fr, fr + 16
+            int fd = 0, fk = 0, ck = 0, cd = 0;
+            auto fetch = [&](int k) {
+                if (k < steps) {
+                    int col = rank + fd;
+                    if (col >= n) col -= n;
+                    const uint32_t dst = ptx::smem_u32(stages + (k % kNsStages) * kNsStage + fr * (kNsK + 4) + fc);
+                    const int k0 = fk * kNsK + fc;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = col * kNsRows + fr + 16 * i;
+                        const bool ok = r < sp && k0 < sp;
+                        ptx::cp_async16(dst + 16 * i * (kNsK + 4) * 8, ok ? X + r * sp + k0 : X, ok ? 16 : 0);
+                    }
+                    if (++fk == nk) { fk = 0; ++fd; }
+                }
+                ptx::cp_async_commit();
+            };
+            double acc[2][1][1][4] = {};          // even and odd steps of eight: two chains of products
+            for (int k = 0; k < kNsStages - 1; ++k) fetch(k);
+            for (int k = 0; k < steps; ++k) {
+                ptx::cp_async_wait<kNsStages - 2>();
+                __syncthreads();                  // the stage is there, and every warp has left the one fetched next
+                fetch(k + kNsStages - 1);
+                const double* const as = G + wr * kNsBigPitch + ck * kNsK;
+                const double* const bs = stages + (k % kNsStages) * kNsStage + wc * (kNsK + 4);
+#pragma unroll
+                for (int q = 0; q < kNsK / 8; ++q)
+                    if (ck * (kNsK / 8) + q < k8) dmma_block(acc[q & 1], as + 8 * q, kNsBigPitch, bs + 8 * q, kNsK + 4, 1);
+                if (++ck < nk) continue;
+                int col = rank + cd;
+                if (col >= n) col -= n;
+                // (the diagonal blocks and those half way round come from both sides: each writes its own)
+                const bool mirror = cd > 0 && 2 * cd != n;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[0][0][0][i] += acc[1][0][0][i];
+                dmma_each(acc[0], [&](int r, int q, double x, double y) {
+                    const int i = r0 + wr + r, j = col * kNsRows + wc + q;
+                    if (i >= sp || j >= sp) return;
+                    x = f(i, j, x);
+                    y = f(i, j + 1, y);
+                    *reinterpret_cast<double2*>(C + i * sp + j) = make_double2(x, y);
+                    if (mirror) {
+                        C[j * sp + i] = x;
+                        C[(j + 1) * sp + i] = y;
+                    }
+                });
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[0][0][0][i] = acc[1][0][0][i] = 0.0;
+                ck = 0;
+                ++cd;
+            }
+            ptx::cp_async_wait<0>();
+            __syncthreads();
+        };
+        auto plain = [](int, int, double v) { return v; };
+        for (int k = 0; k < M.steps; ++k) {
+            const bool last = k + 1 == M.steps;
+            double* const P = k == 0 ? gQ : gP;   // (the first step's P is Q_1)
+            if (work) {
+                if (k > 0) rows_of(gG);
+                product(gG, P, [&](int i, int j, double v) {
+                    return (i == j && i < s ? a : 0.0) + b * G[(i - r0) * kNsBigPitch + j] + c * v;
+                });
+            }
+            sync();
+            if (work && !last) product(P, gR, plain);
+            if (work && k > 0) {
+                rows_of(gQ);
+                product(P, gS, plain);
+            }
+            if (k + 1 < M.steps || k > 0) sync();
+            if (work && !last) {
+                rows_of(gR);
+                product(P, gG, plain);
+            }
+            if (k > 0) {
+                double* const t = gQ;
+                gQ = gS;
+                gS = t;
+            }
+            if (last) break;
+            sync();
+        }
+        if (work) {
+            rows_of(gQ);
+            ptx::cp_async_wait<0>();
+        }
+        __syncthreads();
+    } else if (small) {
+        double* const P = G + kNsSmallS * kNsPitch;
+        auto both = [&](double* C, int i, int j, double v) {
+            C[i * kNsPitch + j] = v;
+            C[j * kNsPitch + i] = v;
+        };
         for (int k = 0; k < M.steps; ++k) {
             // P = a I + b G + c G^2 (the first step's P is Q_1)
             ns_product_small(G, G, sp, [&](int i, int j, double v) {
-                const double p = (i == j && i < s ? a : 0.0) + b * G[i * pitch + j] + c * v;
+                const double p = (i == j && i < s ? a : 0.0) + b * G[i * kNsPitch + j] + c * v;
                 both(P, i, j, p);
                 if (k == 0) both(Q, i, j, p);
             });
@@ -938,46 +1035,83 @@ muon_ns_kernel(const MuonMat* __restrict__ mats, const int32_t* __restrict__ ord
             ns_product_small(P, G, sp, [&](int i, int j, double v) { both(G, i, j, v); });
         }
     } else {
-        double* S = R + sp * sp;
+        const int c0 = warp * 16;                 // this warp's columns
+        const bool work = r0 < s && c0 < s;
+        // The blocks that have rows send theirs, as they lie in their own copy, to each other's.
+        const int active = (s + kNsRows - 1) / kNsRows;
+        constexpr uint32_t kRowsBytes = kNsRows * kNsMidPitch * 8;
+        constexpr int p = kNsMidPitch;
+        double* const F = sm;
+        double* const own = F + r0 * p;
+        uint32_t parity = 0;
+        auto exchange = [&]() {
+            if (rank >= active) return;
+            ptx::fence_proxy_async_smem();
+            __syncthreads();
+            if (tid == 0) {
+                ptx::mbar_arrive_expect_tx(&arrived, (uint32_t)(active - 1) * kRowsBytes);
+                for (int k = 1; k < active; ++k) {
+                    const uint32_t peer = (uint32_t)((rank + k) % active);
+                    ptx::bulk_copy_cluster(ptx::cluster_addr(own, peer), own, kRowsBytes, ptx::cluster_addr(&arrived, peer));
+                }
+            }
+            ptx::mbar_wait_many(&arrived, parity, &abort_flag, timeout_ns, err_flag);
+            parity ^= 1u;
+        };
+        auto put = [&](double* C, const double (&v)[2][2][4]) {
+            dmma_each(v, [&](int r, int q, double x, double y) {
+                *reinterpret_cast<double2*>(C + r * p + c0 + q) = make_double2(x, y);
+            });
+        };
         for (int k = 0; k < M.steps; ++k) {
             const bool last = k + 1 == M.steps;
-            const NsProduct sq{G, G, 0};
-            ns_products(sq, sq, 1, sp, rank, sm, [&](int, int i, int j, double v) {
-                const double p = (i == j && i < s ? a : 0.0) + b * __ldcg(G + i * sp + j) + c * v;
-                both(P, i, j, p);
-                if (k == 0) both(Q, i, j, p);
-            });
-            sync();
-            // Q <- P Q and R = P G together, then G <- P R
-            const NsProduct two0{P, k ? Q : G, k ? 0 : 1}, two1{P, G, 1};
-            const int n2 = (k ? 1 : 0) + (last ? 0 : 1);
-            if (n2 == 0) break;
-            ns_products(two0, two1, n2, sp, rank, sm, [&](int what, int i, int j, double v) { both(what ? R : S, i, j, v); });
-            sync();
-            if (k) { double* t = Q; Q = S; S = t; }
+            double acc[2][2][4] = {};
+            if (work) dmma_block(acc, G, p, F + c0 * p, p, k8);
+            sync();                               // every block has read G: its copies take P
+            if (work) {
+                dmma_each(acc, [&](int r, int q, double x, double y) {
+                    const int i = r0 + r, col = c0 + q;
+                    const double2 g = *reinterpret_cast<const double2*>(G + r * p + col);
+                    x = (i == col && i < s ? a : 0.0) + b * g.x + c * x;
+                    y = (i == col + 1 && i < s ? a : 0.0) + b * g.y + c * y;
+                    *reinterpret_cast<double2*>(own + r * p + col) = make_double2(x, y);
+                    if (k == 0) *reinterpret_cast<double2*>(Q + r * p + col) = make_double2(x, y);
+                });
+            }
+            exchange();
+            double aq[2][2][4] = {};
+            if (work && k > 0) dmma_block(aq, Q, p, F + c0 * p, p, k8);
+            double ar[2][2][4] = {};
+            if (work && !last) dmma_block(ar, G, p, F + c0 * p, p, k8);
+            __syncthreads();
+            if (work && k > 0) put(Q, aq);
+            if (work && !last) put(G, ar);        // R takes G's place
+            __syncthreads();
             if (last) break;
-            const NsProduct pr{P, R, 0};
-            ns_products(pr, pr, 1, sp, rank, sm, [&](int, int i, int j, double v) { both(G, i, j, v); });
-            sync();
+            double ag[2][2][4] = {};
+            if (work) dmma_block(ag, G, p, F + c0 * p, p, k8);
+            sync();                               // every block has read P: its copies take the new G
+            if (work) {
+                put(G, ag);
+                put(own, ag);
+            }
+            exchange();
         }
+        sync();                                   // (no block ends while another copies into it)
     }
-    auto q_of = [&](int r, int c) { return small ? Q[r * pitch + c] : __ldcg(Q + r * sp + c); };
-    // max |Q|: each block's share, then all of them
-    float* const qpart = M.hdr + 2 + M.nchunks * M.npairs;
+    // max |Q|: this block's rows, then all of them
     float qmax = 0.f;
-    for (int e = rank * 256 + tid; e < s2; e += 256 * ranks) qmax = fmaxf(qmax, (float)fabs(q_of(e / s, e % s)));
-    for (int o = 16; o > 0; o >>= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, o));
-    __syncthreads();
-    if ((tid & 31) == 0) redf[tid >> 5] = qmax;
-    __syncthreads();
-    qmax = 0.f;
-    for (int w = 0; w < 8; ++w) qmax = fmaxf(qmax, redf[w]);
+    for (int e = tid; e < nr * s; e += 256)
+        if (r0 + e / s < s) qmax = ptx::max_nan(qmax, (float)fabs(Q[(e / s) * pitch + e % s]));
+    qmax = block_max(qmax);
     if (!small) {
-        if (tid == 0) qpart[rank] = qmax;
+        if (tid < CLUSTER) ptx::st_cluster_f32(ptx::cluster_addr(&qmaxes[rank], tid), qmax);
         sync();
-        for (int k = 0; k < kMuonCluster; ++k) qmax = fmaxf(qmax, __ldcg(qpart + k));
+        qmax = 0.f;
+        for (int k = 0; k < CLUSTER; ++k) qmax = ptx::max_nan(qmax, qmaxes[k]);
+        // (no block ends while another stores into it: all have, before the barrier)
     }
-    const int eq = qmax > 0.f && qmax < 3e38f ? ilogbf(qmax) + 1 : 0, eu = max(big > 0.f ? ilogbf(big) + 1 : -100, -100);
+    const int eq = qmax > 0.f && qmax < 3e38f ? ilogbf(qmax) + 1 : 0, eu = max(umax > 0.f ? ilogbf(umax) + 1 : -100, -100);
     const double qs = scalbn(1.0, 8 - eq);
     if (rank == 0 && tid == 0) {
         M.hdr[0] = scalbnf(1.f, 8 - eu);                                      // x = u hdr[0], |x| < 256
@@ -985,15 +1119,17 @@ muon_ns_kernel(const MuonMat* __restrict__ mats, const int32_t* __restrict__ ord
         const bool fine = tr * 0.0 == 0.0 && qmax < 3e38f;
         M.hdr[1] = fine ? (float)(inv * scalbn(1.0, eu - 8 + eq - 8)) : __int_as_float(0x7fc00000);
     }
-    const int w = s > kMuonBigS ? 256 : 128, kblocks = w / 64;
-    for (int e = rank * 256 + tid; e < w * (w / 8); e += 256 * ranks) {
-        const int r = e / (w / 8), k8 = e - r * (w / 8);
-        const int jr = r / s, cr = r - jr * s;
-        int jk = k8 * 8 / s, ck = k8 * 8 - jk * s;
+    // the parts of this block's rows of the 128 (or 256) that the apply pass takes
+    constexpr int w = BIG ? 256 : 128, kblocks = w / 64;
+    const int rows = small ? w : nr;
+    for (int e = tid; e < rows * (w / 8); e += 256) {
+        const int r = e / (w / 8), k8i = e - r * (w / 8), row = r0 + r;
+        const int jr = row / s, cr = row - jr * s;
+        int jk = k8i * 8 / s, ck = k8i * 8 - jk * s;
         __align__(16) __half h[3][8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const double v = jr < M.J && jr == jk ? q_of(cr, ck) * qs : 0.0;
+            const double v = jr < M.J && jr == jk ? Q[(small ? cr : r) * pitch + ck] * qs : 0.0;
             const double x0 = rint(v);
             h[0][k] = __double2half(x0);
             h[1][k] = __double2half(v - x0);
@@ -1002,7 +1138,7 @@ muon_ns_kernel(const MuonMat* __restrict__ mats, const int32_t* __restrict__ ord
         }
 #pragma unroll
         for (int i = 0; i < 3; ++i)
-            *reinterpret_cast<uint4*>(M.q + muon_q_at(kblocks, r, k8, i)) = *reinterpret_cast<const uint4*>(h[i]);
+            *reinterpret_cast<uint4*>(M.q + muon_q_at(kblocks, row, k8i, i)) = *reinterpret_cast<const uint4*>(h[i]);
     }
 }
 

@@ -1552,7 +1552,9 @@ plora_status backward_call(plora_ctx* h, const void* X, const void* W, const voi
 cudaError_t muon_setup() {
     cudaError_t e = cudaFuncSetAttribute(muon_gram_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGramSmem);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(muon_ns_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMuonNsSmem);
+        e = cudaFuncSetAttribute(muon_ns_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsMidSmem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(muon_ns_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsBigSmem);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(muon_apply_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kApplySmem);
     if (e == cudaSuccess)
@@ -1618,9 +1620,9 @@ void muon_plan(const plora_ctx* h, int32_t n, const plora_adapter* tab, MuonPlan
             M.npairs = ng <= 2 ? 1 : ng * (ng - 1) / 2;
             const size_t s2 = (size_t)M.s * (size_t)M.s, sp = (size_t)round_up(M.s, 8);
             p.part = take(s2 * (size_t)M.nchunks * sizeof(double));
-            if (M.s > kNsSmallS) p.ns = take(5 * sp * sp * sizeof(double));
+            p.ns = take((M.s > kNsMidS ? 5 : 1) * sp * sp * sizeof(double));
             p.q = take((size_t)(big ? 24 : 6) * kMuonPlane);
-            p.hdr = take((size_t)(2 + M.nchunks * M.npairs + kMuonCluster) * sizeof(float));
+            p.hdr = take((size_t)(2 + M.nchunks * M.npairs) * sizeof(float));
             M.gram0 = (int32_t)P.gram_items;
             M.apply0 = (int32_t)P.tiles[big];
             P.gram_items += M.nchunks * M.npairs;
@@ -1721,12 +1723,15 @@ plora_status muon_step(plora_ctx* h, int32_t n, const plora_adapter* tab, const 
     }
     uint8_t *dm = nullptr, *dorder = nullptr;
     int slot = 0;
-    // the iteration's order: matrices that take a cluster first, the largest first
+    // the iteration's order: the largest first
     std::vector<int32_t> order(P.mats.size());
     for (size_t k = 0; k < order.size(); ++k) order[k] = (int32_t)k;
     std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return P.mats[x].s > P.mats[y].s; });
-    int n_cluster = 0;
-    for (const MuonMat& M : P.mats) n_cluster += M.s > kNsSmallS ? 1 : 0;
+    int n_big = 0, n_mid = 0;
+    for (const MuonMat& M : P.mats) {
+        n_big += M.s > kNsMidS ? 1 : 0;
+        n_mid += M.s > kNsSmallS && M.s <= kNsMidS ? 1 : 0;
+    }
     s = upload_parts(h, P.mats.data(), P.mats.size() * sizeof(MuonMat), order.data(), order.size() * sizeof(int32_t), cs,
                      &dm, &dorder, &slot);
     if (s != PLORA_OK) return s;
@@ -1736,21 +1741,30 @@ plora_status muon_step(plora_ctx* h, int32_t n, const plora_adapter* tab, const 
     tracked(h, kMuonGramK, cs, [&] {
         muon_gram_kernel<<<(unsigned)P.gram_items, kGramThreads, kGramSmem, cs>>>(mats, nm, err, kTimeoutNs);
     });
-    const int clusters = n_cluster + (int)ceil_div(nm - n_cluster, kMuonCluster);
-    tracked(h, kMuonNsK, cs, [&] {
-        // clusters spread over the SMs rather than two blocks of one cluster sharing an SM
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterSchedulingPolicyPreference;
-        attr[0].val.clusterSchedulingPolicyPreference = cudaClusterSchedulingPolicySpread;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)clusters * kMuonCluster);
-        cfg.blockDim = dim3(256);
-        cfg.dynamicSmemBytes = kMuonNsSmem;
-        cfg.stream = cs;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        cudaLaunchKernelEx(&cfg, muon_ns_kernel, mats, (const int32_t*)dorder, n_cluster, nm);
-    });
+    tracked(h, kMuonNsK, cs, [&] { muon_sum_kernel<<<(unsigned)nm * kSumBlocks, 256, 0, cs>>>(mats); });
+    // clusters spread over the SMs rather than two blocks of one cluster sharing an SM
+    auto iterate = [&](auto kernel, int at, int count, int mid, int cluster, int blocks, int smem) {
+        tracked(h, kMuonNsK, cs, [&] {
+            cudaLaunchAttribute attr[2];
+            attr[0].id = cudaLaunchAttributeClusterSchedulingPolicyPreference;
+            attr[0].val.clusterSchedulingPolicyPreference = cudaClusterSchedulingPolicySpread;
+            attr[1].id = cudaLaunchAttributeClusterDimension;
+            attr[1].val.clusterDim.x = (unsigned)cluster;
+            attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3((unsigned)round_up(blocks, cluster));
+            cfg.blockDim = dim3(256);
+            cfg.dynamicSmemBytes = (size_t)smem;
+            cfg.stream = cs;
+            cfg.attrs = attr;
+            cfg.numAttrs = 2;
+            cudaLaunchKernelEx(&cfg, kernel, mats, reinterpret_cast<const int32_t*>(dorder) + at, mid, count, err, kTimeoutNs);
+        });
+    };
+    if (n_big > 0) iterate(muon_ns_kernel<true>, 0, n_big, n_big, kNsBigCluster, n_big * kNsBigCluster, kNsBigSmem);
+    if (nm > n_big)
+        iterate(muon_ns_kernel<false>, n_big, nm - n_big, n_mid, kNsMidCluster,
+                n_mid * kNsMidCluster + (nm - n_big - n_mid), n_mid > 0 ? kNsMidSmem : kNsSmallSmem);
     const int32_t ns = P.n_small;
     if (ns > 0)
         tracked(h, kMuonApplyK, cs, [&] {
