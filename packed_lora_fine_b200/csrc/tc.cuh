@@ -735,7 +735,7 @@ __device__ __forceinline__ void epilogue_store_ep(const CUtensorMap* tmY, const 
         if (ep.want_z) put(tmZ, z, col0);
         with_act(ep.act, [&](auto ACT) {
 #pragma unroll
-            for (int k = 0; k < 64; ++k) z[k] = act_fwd<ACT.value>(z[k]);
+            for (int k = 0; k < 64; ++k) z[k] = act_fwd<__nv_bfloat16, ACT.value>(z[k]);
         });
         if (res) {
 #pragma unroll

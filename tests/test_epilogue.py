@@ -300,6 +300,42 @@ def test_activations_at_their_borders():
 
 
 @gpu
+@pytest.mark.parametrize("act", ACTS)
+def test_bf16_activations_at_their_borders(act):
+    # as above: rounded once, the functions within 2^-21 of |z| and the derivatives within 2^-19 absolute.
+    # The fast exponential is off by (2 + 1.16 |x|) ulps and the fast division by 2, of terms z^k exp(-|z|) and
+    # z^k exp(-z^2 / 2) whose (1 + |x|)-fold stays below 4; erf's polynomial by 1.5e-7
+    vals = torch.cat([torch.linspace(-12, 12, 113), torch.tensor([0.0, -0.0, 1e-30, -1e-30, 30.0, -30.0, 60.0, -60.0, 100.0,
+                      -100.0, 1e4, -1e4, 1e30, -1e30, math.inf, math.nan])]).bfloat16()
+    n = (vals.numel() + 7) // 8 * 8
+    vals = torch.cat([vals, torch.zeros(n - vals.numel(), dtype=torch.bfloat16)])
+    p = Problem("bf16", 16, n, [2], [3], residual=False, seed=10)
+    p.X.zero_()
+    p.bias = [vals.cuda()]
+    eng = p.engine()
+    Y, saved, Z = eng.forward_epilogue(p.X, p.W, p.off, p.scales, p.A, p.B, bias=p.bias, activation=act)
+    ref = act64(vals.double(), act)
+    got = Y[0].double().cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    ok = torch.isfinite(ref)
+    assert torch.equal(got[~ok & ~torch.isnan(ref)], ref[~ok & ~torch.isnan(ref)])
+    assert ((got - ref).abs()[ok] <= U * ref.abs()[ok] + 2.0 ** -21 * vals.double().abs()[ok].clamp(max=100.0)).all()
+    if act != "none":
+        db = eng.backward_epilogue(p.X, p.W, torch.ones_like(Y), p.off, p.scales, p.A, p.B, saved, Z=Z, activation=act,
+                                   want_dbias=True)[3]
+        q = vals.double().clone().requires_grad_(True)
+        fin = torch.isfinite(vals) & (vals.abs() <= 1e4)
+        g, = torch.autograd.grad(act64(q[fin], act).sum(), q)
+        if act == "relu":
+            g[vals == 0] = 0.0
+        got = db[0].double().cpu() / 3
+        assert ((got - g).abs()[fin] <= 2.0 ** -19).all()
+        far = vals.abs() == torch.tensor(1e30).bfloat16()
+        assert torch.equal(got[far], (vals[far] > 0).double())
+    eng.close()
+
+
+@gpu
 def test_gradients_against_differences():
     p = Problem("fp32", 24, 40, [3, 2], [6, 5], seed=11)
     eng = p.engine()
