@@ -229,7 +229,7 @@ typedef enum {
 } plora_activation;
 
 /*
- * activation: a plora_activation; reserved: 0.  bias, dbias: HOST arrays of n_adapters device pointers,
+ * activation: a plora_activation; inference: 0 or 1.  bias, dbias: HOST arrays of n_adapters device pointers,
  * or NULL; an entry may be NULL (no bias, no gradient wanted).  bias[i]: [d_out] in the handle's dtype;
  * dbias[i]: [d_out] fp32, overwritten (zero for an adapter without tokens).  residual: [T][d_out] in the
  * handle's dtype or NULL; with a bf16 handle it may be Y itself (added in place).  Z: [T][d_out] in the handle's dtype:
@@ -238,10 +238,14 @@ typedef enum {
  * ignores dbias and work, the backward bias and residual (dR is dY).  Every other pointer is 16-byte
  * aligned.  A buffer that a call writes must not overlap another of these buffers, Y, dY or dX
  * (PLORA_ERR_INVALID_ARG), except residual = Y.
+ * inference 1: a forward without a backward.  Z is NULL, and `saved`, of plora_saved_bytes() as ever, is scratch
+ * that holds nothing afterwards.  With a bf16 handle and at most 32 tokens such a call reads W once in kernels for
+ * few tokens, takes no schedule slot (a capture needs none reserved for it) and sums in another order than a
+ * training call; a token's result does not depend on the call's other tokens within 32, or above.
  */
 typedef struct {
     int32_t activation;
-    int32_t reserved;
+    int32_t inference;
     const void* const* bias;
     float* const* dbias;
     const void* residual;

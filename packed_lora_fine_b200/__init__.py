@@ -92,7 +92,7 @@ class plora_adamw_state(ctypes.Structure):
 
 
 class plora_epilogue(ctypes.Structure):
-    _fields_ = [("activation", ctypes.c_int32), ("reserved", ctypes.c_int32), ("bias", ctypes.c_void_p),
+    _fields_ = [("activation", ctypes.c_int32), ("inference", ctypes.c_int32), ("bias", ctypes.c_void_p),
                 ("dbias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("Z", ctypes.c_void_p),
                 ("work", ctypes.c_void_p)]
 
@@ -430,7 +430,8 @@ def plora_muon_step(h: int, n: int, tab, states, work: int, stream: int = 0, che
     return s
 
 
-def make_epilogue(activation="none", bias=None, dbias=None, residual=None, Z=None, work=None) -> plora_epilogue:
+def make_epilogue(activation="none", bias=None, dbias=None, residual=None, Z=None, work=None,
+                  inference=False) -> plora_epilogue:
     """plora_epilogue from an activation's name (or number) and device pointers (ints); bias and dbias are
     lists with one pointer (or None) per adapter, or None."""
     ep = plora_epilogue()
@@ -444,6 +445,7 @@ def make_epilogue(activation="none", bias=None, dbias=None, residual=None, Z=Non
             keep.append(arr)
             setattr(ep, name, ctypes.addressof(arr))
     ep.residual, ep.Z, ep.work = residual or None, Z or None, work or None
+    ep.inference = int(inference)
     ep._keep = keep
     return ep
 
@@ -597,8 +599,9 @@ class PackedLoRA:
         bias: one ``[d_out]`` tensor for every adapter, a list with one (or None) per adapter, or None;
         activation: a name in ``ACTIVATIONS``; residual: ``[T][d_out]`` (with a bf16 engine it may be the tensor
         given as Y).
-        Z, the pre-activation that ``backward_epilogue`` needs, is kept if there is an activation and
-        want_Z is true, else None."""
+        Z is the pre-activation that ``backward_epilogue`` needs with an activation (None without one).
+        want_Z false: an inference call, which keeps nothing for a backward.  saved and Z are then None, and up to 32
+        tokens of a bf16 engine go through kernels for few tokens (sums in another order than a training call's)."""
         import torch
         n = len(off) - 1
         self._check_tensors(X.shape[0], X=X, W=W, residual=residual, Y=Y)
@@ -612,10 +615,10 @@ class PackedLoRA:
         Z = torch.empty_like(Y) if want_Z and activation != "none" else None
         ep = make_epilogue(activation, None if bias is None else [b.data_ptr() if b is not None else None for b in bias],
                            residual=residual.data_ptr() if residual is not None else None,
-                           Z=Z.data_ptr() if Z is not None else None)
+                           Z=Z.data_ptr() if Z is not None else None, inference=not want_Z)
         st = (stream or torch.cuda.current_stream(X.device)).cuda_stream
         plora_forward_epilogue(self.h, X.data_ptr(), W.data_ptr(), Y.data_ptr(), n, off, tab, saved.data_ptr(), ep, st)
-        return Y, saved, Z
+        return Y, saved if want_Z else None, Z
 
     def backward_epilogue(self, X, W, dY, off, scales, A, B, saved, Z=None, activation="none", want_dX=True,
                           want_dbias=False, stream=None):

@@ -25,6 +25,7 @@
 #include "tc_pair.cuh"
 #include "adamw.cuh"
 #include "epilogue.cuh"
+#include "few.cuh"
 #include "muon.cuh"
 
 using namespace plora;
@@ -225,12 +226,12 @@ __global__ void timeout_probe_kernel(int* err_flag, uint64_t limit_ns) {
 
 // Kernel kinds for launch accounting / profiling.
 enum Kind { kPack = 0, kBaseFwd, kShrinkX, kExpandY, kBaseDx, kShrinkDy, kExpandDx, kWgradB, kWgradA,
-            kSimt, kAdamw, kShrinkDyWgradB, kStage, kBaseDxWgradA, kBaseFwdEp, kEpilogue, kActGrad, kBiasGrad,
-            kMuonGramK, kMuonNsK, kMuonApplyK, kKinds };
+            kSimt, kAdamw, kShrinkDyWgradB, kStage, kBaseDxWgradA, kBaseFwdEp, kFewShrink,
+            kFewBase, kEpilogue, kActGrad, kBiasGrad, kMuonGramK, kMuonNsK, kMuonApplyK, kKinds };
 const char* const kKindNames[kKinds] = {"pack_ab", "base_fwd", "shrink_x", "expand_y", "base_dx",
                                         "shrink_dy", "expand_dx", "wgrad_b", "wgrad_a", "simt_gemm", "adamw",
                                         "shrink_dy+wgrad_b", "stage_copy", "base_dx+wgrad_a", "base_fwd_ep",
-                                        "epilogue", "act_grad", "bias_grad", "muon_gram", "muon_ns", "muon_apply"};
+                                        "few_shrink", "few_base", "epilogue", "act_grad", "bias_grad", "muon_gram", "muon_ns", "muon_apply"};
 static_assert(kKinds <= 32, "plora_ctx::launches and total_ms hold every kind");
 
 cudaEvent_t take_event(plora_ctx* h) {
@@ -486,6 +487,7 @@ struct DevPlan {
 struct EpiTables {
     bool on = false;
     int32_t act = 0;
+    bool inference = false;
     const void* residual = nullptr;
     void* Z = nullptr;
     void* work = nullptr;
@@ -1335,12 +1337,15 @@ plora_status epilogue_args(plora_ctx* h, const HostPlan& P, const plora_epilogue
         return fail(h, PLORA_ERR_UNSUPPORTED, "an epilogue needs an fp32 handle or the tensor-core path");
     if (h->cfg.flags & (PLORA_FLAG_UNFUSED | PLORA_FLAG_BASE_PAIR))
         return fail(h, PLORA_ERR_UNSUPPORTED, "an epilogue needs the fused single-SM base GEMM");
-    if (e.activation < PLORA_ACT_NONE || e.activation > PLORA_ACT_SILU || e.reserved != 0)
-        return fail(h, PLORA_ERR_INVALID_ARG, "activation=%d, reserved=%d", e.activation, e.reserved);
+    if (e.activation < PLORA_ACT_NONE || e.activation > PLORA_ACT_SILU || e.inference < 0 || e.inference > 1)
+        return fail(h, PLORA_ERR_INVALID_ARG, "activation=%d, inference=%d", e.activation, e.inference);
     const bool act = e.activation != PLORA_ACT_NONE;
     const size_t es = h->esize, d_out = (size_t)h->cfg.d_out, ybytes = (size_t)P.T * d_out * es;
+    if (e.inference && (backward || e.Z))
+        return fail(h, PLORA_ERR_INVALID_ARG, "an inference call has no backward: Z is NULL");
     ep.on = true;
     ep.act = e.activation;
+    ep.inference = e.inference != 0;
     std::vector<Span> spans;
     auto buffer = [&](const void* p, size_t bytes, size_t align, bool write, const char* name) {
         if ((reinterpret_cast<uintptr_t>(p) & (align - 1)) != 0)
@@ -1406,6 +1411,61 @@ plora_status epilogue_args(plora_ctx* h, const HostPlan& P, const plora_epilogue
     return PLORA_OK;
 }
 
+// The inference forward over at most kFewTokens tokens: two launches, the second's blocks beginning as the first's
+// end.  The call's tables travel as kernel parameters, so no schedule slot is taken.  `saved` holds H.
+template <int NT> void few_launch(plora_ctx* h, const FewArgs& a, int tiles, cudaStream_t st) {
+    tracked(h, kFewShrink, st, [&] { few_shrink_kernel<NT><<<(unsigned)tiles, 256, 0, st>>>(a); });
+    tracked(h, kFewBase, st, [&] {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)ceil_div(a.d_out, kFewRows));
+        cfg.blockDim = dim3(256);
+        cfg.stream = st;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        cudaLaunchKernelEx(&cfg, few_base_kernel<NT>, a);
+    });
+}
+plora_status few_forward(plora_ctx* h, const void* X, const void* W, void* Y, const HostPlan& P, void* saved,
+                         const EpiTables& ep, cudaStream_t st) {
+    FewArgs a{};
+    a.X = static_cast<const __nv_bfloat16*>(X);
+    a.W = static_cast<const __nv_bfloat16*>(W);
+    a.residual = static_cast<const __nv_bfloat16*>(ep.residual);
+    a.Y = static_cast<__nv_bfloat16*>(Y);
+    a.H = static_cast<float*>(saved);
+    a.d_in = h->cfg.d_in;
+    a.d_out = h->cfg.d_out;
+    a.T = (int32_t)P.T;
+    a.RP = P.RP;
+    a.act = ep.act;
+    a.blocks.n = h->nblk;
+    for (int b = 0; b < h->nblk; ++b) a.blocks.end[b] = (int32_t)h->blk_end[b];
+    int tiles = 0;
+    for (int32_t i = 0; i < P.n; ++i) {
+        const AdapterDev& d = P.ad[i];
+        if (d.n == 0) continue;
+        for (int32_t t = 0; t < d.n; ++t) a.owner[d.x_row + t] = (uint8_t)a.n;
+        FewAdapter& f = a.ad[a.n++];
+        f.A = static_cast<const __nv_bfloat16*>(d.A);
+        f.B = static_cast<const __nv_bfloat16*>(d.B);
+        f.bias = ep.bias.empty() ? nullptr : static_cast<const __nv_bfloat16*>(ep.bias[i]);
+        f.scale = d.scale;
+        f.rank = d.rank;
+        f.x_row = d.x_row;
+        f.n = d.n;
+        f.tile0 = tiles;
+        tiles += (int)ceil_div((int64_t)h->nblk * d.rank, kFewRows);
+    }
+    if (a.T <= 8) few_launch<1>(h, a, tiles, st);
+    else if (a.T <= 16) few_launch<2>(h, a, tiles, st);
+    else few_launch<4>(h, a, tiles, st);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? PLORA_OK : cuda_fail(h, e, "kernel launch");
+}
+
 // plora_forward, with an epilogue if epi is not null.
 plora_status forward_call(plora_ctx* h, const void* X, const void* W, void* Y, int32_t n, const int64_t* off,
                           const plora_adapter* tab, void* saved, const plora_epilogue* epi, void* stream) {
@@ -1455,6 +1515,8 @@ plora_status forward_call(plora_ctx* h, const void* X, const void* W, void* Y, i
         if (ep.on) epilogue_apply<float>(h, P, D, ep, Y, st);   // an epilogue needs an fp32 handle here
         return finish(h, D, st);
     }
+
+    if (ep.inference && P.T <= kFewTokens) return few_forward(h, X, W, Y, P, saved, ep, st);
 
     // Tensor-core path.
     FwdCall c;
@@ -2029,8 +2091,8 @@ plora_status plora_epilogue_work_bytes(plora_handle h, int32_t n, const int64_t*
     if (!bytes) return fail(h, PLORA_ERR_INVALID_ARG, "bytes is NULL");
     *bytes = 0;
     if (!ep) return fail(h, PLORA_ERR_INVALID_ARG, "the epilogue is NULL");
-    if (ep->activation < PLORA_ACT_NONE || ep->activation > PLORA_ACT_SILU || ep->reserved != 0)
-        return fail(h, PLORA_ERR_INVALID_ARG, "activation=%d, reserved=%d", ep->activation, ep->reserved);
+    if (ep->activation < PLORA_ACT_NONE || ep->activation > PLORA_ACT_SILU || ep->inference < 0 || ep->inference > 1)
+        return fail(h, PLORA_ERR_INVALID_ARG, "activation=%d, inference=%d", ep->activation, ep->inference);
     const plora_status s = check_offsets(h, n, off);
     if (s != PLORA_OK) return s;
     int64_t tiles = 0;

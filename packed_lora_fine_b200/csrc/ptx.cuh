@@ -405,6 +405,10 @@ __device__ __forceinline__ void bulk_copy_cluster(uint32_t dst, const void* src,
                  ::"r"(dst), "r"(smem_u32(src)), "r"(bytes), "r"(bar) : "memory");
 }
 
+// Programmatic launch: lets the next launch's blocks start, and waits for the one before to end.
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Named barrier among the `nthreads` threads that use id `id` (id 0 is __syncthreads).
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");

@@ -444,6 +444,92 @@ def test_capture_replays_and_runs_on_another_stream():
     eng.close()
 
 
+# ------------------------------------------------------------------ inference, a few tokens
+def infer(p, eng, act, residual=True, **kw):
+    Y, saved, Z = eng.forward_epilogue(p.X[:p.T], p.W, p.off, p.scales, p.A, p.B, bias=p.bias, activation=act, want_Z=False,
+                                       residual=p.R[:p.T] if residual and p.R is not None else None, **kw)
+    assert saved is None and Z is None
+    return Y
+
+
+FEW = [
+    # d_in, d_out, ranks, counts, output blocks: one token; eight; nine; ranks that are no multiple of 8, adapters
+    # without tokens, columns past a block's 16; K ending inside a slice; the most tokens; one more than that
+    (64, 8, [1], [1], 1),
+    (136, 264, [4, 17, 64], [1, 0, 7], 1),
+    (1000, 520, [128, 200], [5, 4], 1),
+    (200, 768, [8, 24, 3], [2, 0, 14], 3),
+    (72, 1032, [2] * 20, [1, 2] * 10, 1),
+    (4104, 136, [16, 256], [1, 31], 1),
+    (136, 264, [4, 17], [1, 32], 1),
+]
+
+
+@gpu
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("k", range(len(FEW)))
+def test_few_tokens_match_the_formulas(k, act):
+    d_in, d_out, ranks, counts, blocks = FEW[k]
+    p = Problem("bf16", d_in, d_out, ranks, counts, blocks=blocks, bias=("each", "some", "shared")[k % 3], residual=k % 2 == 0,
+                seed=20 + k)
+    eng = p.engine()
+    Y = infer(p, eng, act)
+    assert pl.plora_check(eng.h, 0) == pl.PLORA_OK
+    ref = p.reference(act)
+    b = bounds(p, ref, None, act, (max(d_in, max(ranks)) + 8) * 2.0 ** -24 + U)
+    assert inside(Y, ref["Y"], b["Y"])
+    assert torch.equal(Y, infer(p, eng, act))
+    eng.close()
+
+
+@gpu
+def test_few_tokens_alone_in_place_and_captured():
+    p = Problem("bf16", 264, 392, [16, 3, 40], [9, 1, 15], extra=5, seed=30)
+    eng = p.engine()
+    Y = infer(p, eng, "silu")
+    for i in range(p.n):               # an adapter's rows alone, which take another number of tokens at a time
+        s = slice(int(p.off[i]), int(p.off[i + 1]))
+        y, _, _ = eng.forward_epilogue(p.X[s].contiguous(), p.W, np.array([0, s.stop - s.start]), p.scales[i:i + 1],
+                                       p.A[i:i + 1], p.B[i:i + 1], bias=p.bias[i:i + 1], activation="silu",
+                                       residual=p.R[s].contiguous(), want_Z=False)
+        assert torch.equal(y, Y[s])
+    R = p.R.clone()                    # the residual is Y itself; rows behind the last adapter stay
+    eng.forward_epilogue(p.X, p.W, p.off, p.scales, p.A, p.B, bias=p.bias, activation="silu", residual=R, Y=R, want_Z=False)
+    assert torch.equal(R[:p.T], Y) and torch.equal(R[p.T:], p.R[p.T:])
+    out, saved = torch.empty_like(Y), torch.empty(eng.saved_bytes(p.off, eng.table(p.scales, p.A, p.B)), dtype=torch.uint8,
+                                                  device="cuda")
+    graph = torch.cuda.CUDAGraph()     # no schedule slot is reserved
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        infer(p, eng, "silu", Y=out, saved=saved)
+        infer(p, eng, "silu", Y=out, saved=saved)
+    p.X.neg_()
+    graph.replay()
+    want = infer(p, eng, "silu")
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and not torch.equal(out, Y)
+    del graph
+    eng.close()
+
+
+@gpu
+def test_inference_keeps_nothing():
+    p = Problem("bf16", 72, 264, [8, 5], [40, 30], seed=31)      # more than a few tokens: the training kernels
+    eng = p.engine()
+    Y, _, Z = eng.forward_epilogue(p.X, p.W, p.off, p.scales, p.A, p.B, bias=p.bias, activation="gelu", residual=p.R)
+    assert torch.equal(infer(p, eng, "gelu"), Y)
+    tab, saved = eng.table(p.scales, p.A, p.B), torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    ep = pl.make_epilogue("gelu", Z=Z.data_ptr(), inference=True)
+    assert pl.plora_forward_epilogue(eng.h, p.X.data_ptr(), p.W.data_ptr(), Y.data_ptr(), 2, p.off, tab, saved.data_ptr(), ep, 0,
+                                     check=False) == pl.PLORA_ERR_INVALID_ARG
+    eng.close()
+    p = Problem("fp32", 72, 264, [8, 5], [4, 3], seed=32)
+    eng = p.engine()
+    Y, _, _ = eng.forward_epilogue(p.X, p.W, p.off, p.scales, p.A, p.B, bias=p.bias, activation="gelu", residual=p.R)
+    assert torch.equal(infer(p, eng, "gelu"), Y)
+    eng.close()
+
+
 # ------------------------------------------------------------------ autograd
 @gpu
 @pytest.mark.parametrize("shared", [False, True])
@@ -530,8 +616,8 @@ def test_refusals_leave_the_outputs_alone():
                m("gelu", residual=Z.data_ptr(), Z=Z.data_ptr())):
         assert fwd(ep) == bad
     ep = m("gelu")
-    ep.reserved = 1
-    assert fwd(ep) == bad and "reserved" in pl.plora_last_error(eng.h)
+    ep.inference = 2
+    assert fwd(ep) == bad and "inference" in pl.plora_last_error(eng.h)
     dbp = [b.data_ptr() for b in db]
     for ep in (m("gelu", work=work.data_ptr()),                                        # no Z
                m("gelu", Z=Z.data_ptr()),                                              # no work
