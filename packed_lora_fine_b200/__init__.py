@@ -13,7 +13,10 @@ raises ``ImportError``.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
+import functools
+import math
 import os
 from typing import Iterable, List, Optional, Sequence
 
@@ -205,15 +208,10 @@ def make_table(ranks: Sequence[int], scales: Sequence[float], A: Sequence[int], 
                dA: Optional[Sequence[int]] = None, dB: Optional[Sequence[int]] = None):
     """Build a host plora_adapter[] from ranks, scales and device pointers (ints)."""
     n = len(ranks)
-    tab = (plora_adapter * max(1, n))()
-    for i in range(n):
-        tab[i].rank = int(ranks[i])
-        tab[i].scale = float(scales[i])
-        tab[i].A = int(A[i])
-        tab[i].B = int(B[i])
-        tab[i].dA = int(dA[i]) if dA is not None else None
-        tab[i].dB = int(dB[i]) if dB is not None else None
-    return tab
+    none = (None,) * n
+    return (plora_adapter * max(1, n))(*[
+        (int(r), float(s), int(a), int(b), None if da is None else int(da), None if db is None else int(db))
+        for r, s, a, b, da, db in zip(ranks, scales, A, B, none if dA is None else dA, none if dB is None else dB)])
 
 
 # ---------------------------------------------------------------- C names
@@ -564,7 +562,7 @@ class PackedLoRA:
             if t is None:
                 continue
             want = shape.get(name, (T, self.d_out))
-            if tuple(t.shape) != want or t.dtype != dt or not t.is_contiguous():
+            if t.shape != want or t.dtype != dt or not t.is_contiguous():
                 raise ValueError(f"{name}: a contiguous {dt} tensor of shape {want} is needed, got {t.dtype} "
                                  f"{tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous'}")
 
@@ -576,7 +574,7 @@ class PackedLoRA:
             raise ValueError(f"{len(A)} A and {len(B)} B factors for {n} adapters")
         for i, (a, b) in enumerate(zip(A, B)):
             r = b.shape[1]
-            if tuple(a.shape) != (P * r, self.d_in) or tuple(b.shape) != (self.d_out, r) or a.dtype != dt \
+            if a.shape != (P * r, self.d_in) or b.shape != (self.d_out, r) or a.dtype != dt \
                     or b.dtype != dt or not a.is_contiguous() or not b.is_contiguous():
                 raise ValueError(f"adapter {i}: contiguous {dt} factors A {(P * r, self.d_in)} and B "
                                  f"{(self.d_out, r)} are needed, got {tuple(a.shape)} and {tuple(b.shape)}")
@@ -588,7 +586,7 @@ class PackedLoRA:
         out = list(bias) if isinstance(bias, (list, tuple)) else [bias] * n
         if len(out) != n:
             raise ValueError(f"bias: {len(out)} entries for {n} adapters")
-        for b in out:
+        for b in out if isinstance(bias, (list, tuple)) else [bias]:
             self._check_tensors(0, bias=b)
         return out
 
@@ -621,8 +619,10 @@ class PackedLoRA:
         return Y, saved if want_Z else None, Z
 
     def backward_epilogue(self, X, W, dY, off, scales, A, B, saved, Z=None, activation="none", want_dX=True,
-                          want_dbias=False, stream=None):
-        """The backward of ``forward_epilogue``: returns (dX, dA, dB, dbias).  dX is None without want_dX;
+                          want_dbias=False, stream=None, dA=None, dB=None, dbias=None):
+        """The backward of ``forward_epilogue``: returns (dX, dA, dB, dbias).  dX is None without want_dX; dA and dB
+        may be given together, and dbias in place of want_dbias: lists of 16-byte aligned contiguous fp32 tensors of A's,
+        B's and the biases' shapes (dbias: or None for an adapter).
         dbias is a list of fp32 ``[d_out]`` tensors, one per adapter, or None; want_dbias may be a list of
         truth values, one per adapter (dbias[i] is then None where it is false).  The residual's gradient
         is dY."""
@@ -631,10 +631,11 @@ class PackedLoRA:
         self._check_tensors(X.shape[0], X=X, W=W, dY=dY, Z=Z)
         self._check_factors(A, B, n)
         f32 = dict(dtype=torch.float32, device=X.device)
-        dA, dB = [torch.empty(a.shape, **f32) for a in A], [torch.empty(b.shape, **f32) for b in B]
+        if dA is None and dB is None:
+            dA, dB = [torch.empty(a.shape, **f32) for a in A], [torch.empty(b.shape, **f32) for b in B]
         dX = torch.empty_like(X) if want_dX else None
         want = list(want_dbias) if isinstance(want_dbias, (list, tuple)) else [bool(want_dbias)] * n
-        db = [torch.empty(self.d_out, **f32) if w else None for w in want] if any(want) else None
+        db = dbias if dbias is not None else [torch.empty(self.d_out, **f32) if w else None for w in want] if any(want) else None
         tab = self.table(scales, A, B, dA, dB)
         ep = make_epilogue(activation, dbias=None if db is None else [b.data_ptr() if b is not None else None for b in db],
                            Z=Z.data_ptr() if Z is not None else None)
@@ -768,6 +769,70 @@ class PackedLoRALayer:
 
 
 # ---------------------------------------------------------------- autograd
+# What a packed_lora call holds besides its tensors; where[i] is adapter i's place among the distinct biases.
+_Call = collections.namedtuple("_Call", "engine off scales n plain where activation")
+
+
+@functools.lru_cache(maxsize=None)
+def _packed_lora_fn():
+    """packed_lora's autograd function (made once, on first use: the module does not import torch)."""
+    import torch
+
+    class PackedLoRAFn(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, call, X_, W_, R_, *ABb):
+            n = call.n
+            A_, B_, b_ = list(ABb[:n]), list(ABb[n:2 * n]), ABb[2 * n:]
+            X_, W_, Z = X_.contiguous(), W_.contiguous(), None
+            if call.plain:
+                Y, saved = call.engine.forward(X_, W_, call.off, call.scales, A_, B_)
+            else:
+                Y, saved, Z = call.engine.forward_epilogue(X_, W_, call.off, call.scales, A_, B_,
+                                                           bias=[None if k is None else b_[k] for k in call.where],
+                                                           activation=call.activation,
+                                                           residual=None if R_ is None else R_.contiguous())
+            ctx.call = call
+            ctx.save_for_backward(X_, W_, saved, Z, *ABb[:2 * n])
+            return Y
+
+        @staticmethod
+        def backward(ctx, dY):
+            call, n = ctx.call, ctx.call.n
+            X_, W_, saved, Z, *AB = ctx.saved_tensors
+            A_, B_ = list(AB[:n]), list(AB[n:])
+            need_b = ctx.needs_input_grad[4 + 2 * n:]
+            want_dX = ctx.needs_input_grad[1]
+            gb = [None] * len(need_b)
+            # the fp32 gradients lie in one buffer, so that one launch casts them
+            want_db = [k is not None and need_b[k] for k in call.where]
+            shapes = [t.shape for t in AB] + [(dY.shape[1],)] * sum(want_db)
+            counts = [math.prod(s) for s in shapes]
+            sizes = [-(-c // 64) * 64 for c in counts]
+
+            def cut(buf):
+                return [g[:c].view(s) for g, c, s in zip(buf.split(sizes), counts, shapes)] if sizes else []
+            flat = torch.empty(sum(sizes), dtype=torch.float32, device=dY.device)
+            g32 = cut(flat)
+            grads = dict(dA=g32[:n], dB=g32[n:2 * n], want_dX=want_dX)
+            if call.plain:
+                dX, _, _ = call.engine.backward(X_, W_, dY.contiguous(), call.off, call.scales, A_, B_, saved, **grads)
+            else:
+                rest = iter(g32[2 * n:])
+                dX, _, _, _ = call.engine.backward_epilogue(X_, W_, dY.contiguous(), call.off, call.scales, A_, B_, saved, Z=Z,
+                                                            activation=call.activation, **grads,
+                                                            dbias=[next(rest) if w else None for w in want_db]
+                                                            if any(want_db) else None)
+            g = cut(flat.to(dY.dtype)) if dY.dtype != flat.dtype else g32
+            for k, need in enumerate(need_b):       # a shared bias sums its adapters' fp32 gradients
+                if need:
+                    own = [2 * n + sum(want_db[:i]) for i in range(n) if call.where[i] == k]
+                    gb[k] = g[own[0]] if len(own) == 1 else torch.stack([g32[j] for j in own]).sum(0).to(dY.dtype)
+            g = g[:2 * n]
+            return (None, dX, None, dY if ctx.needs_input_grad[3] else None, *g, *gb)
+
+    return PackedLoRAFn
+
+
 def packed_lora(engine: "PackedLoRA", X, W, off, scales, A, B, bias=None, activation="none", residual=None):
     """Y = act(X W + s_i (X_i A_i) B_i + b_i) + residual for every packed adapter, differentiable in X,
     A_i, B_i, b_i and residual (W is the frozen base weight and gets no gradient).  A[i] is lora_A.weight
@@ -776,49 +841,13 @@ def packed_lora(engine: "PackedLoRA", X, W, off, scales, A, B, bias=None, activa
     shares (its gradient sums over the adapters) or a list with one (or None) per adapter; activation: a
     name in ACTIVATIONS; residual: [T][d_out].  Without these three the backward runs plora_backward, else
     plora_backward_epilogue; the fp32 weight gradients are returned in each parameter's dtype."""
-    import torch
     n = len(off) - 1
     plain = bias is None and activation == "none" and residual is None
     per_adapter = [None] * n if bias is None else engine._bias_list(bias, n)
     uniq = list({id(b): b for b in per_adapter if b is not None}.values())   # a shared bias is one input
     where = [next((k for k, u in enumerate(uniq) if u is b), None) for b in per_adapter]
 
-    class _PackedLoRAFn(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, X_, W_, R_, *ABb):
-            A_, B_, b_ = list(ABb[:n]), list(ABb[n:2 * n]), ABb[2 * n:]
-            X_, W_, Z = X_.contiguous(), W_.contiguous(), None
-            if plain:
-                Y, saved = engine.forward(X_, W_, off, scales, A_, B_)
-            else:
-                Y, saved, Z = engine.forward_epilogue(X_, W_, off, scales, A_, B_,
-                                                      bias=[None if k is None else b_[k] for k in where],
-                                                      activation=activation,
-                                                      residual=None if R_ is None else R_.contiguous())
-            ctx.save_for_backward(X_, W_, saved, Z, *ABb[:2 * n])
-            return Y
-
-        @staticmethod
-        def backward(ctx, dY):
-            X_, W_, saved, Z, *AB = ctx.saved_tensors
-            A_, B_ = list(AB[:n]), list(AB[n:])
-            need_b = ctx.needs_input_grad[3 + 2 * n:]
-            gb = [None] * len(uniq)
-            if plain:
-                dX, dA, dB = engine.backward(X_, W_, dY.contiguous(), off, scales, A_, B_, saved,
-                                             want_dX=ctx.needs_input_grad[0])
-            else:
-                dX, dA, dB, db = engine.backward_epilogue(X_, W_, dY.contiguous(), off, scales, A_, B_, saved, Z=Z,
-                                                          activation=activation, want_dX=ctx.needs_input_grad[0],
-                                                          want_dbias=[k is not None and need_b[k] for k in where])
-                for k, u in enumerate(uniq):   # a shared bias sums its adapters' fp32 gradients
-                    if need_b[k]:
-                        own = [db[i] for i in range(n) if where[i] == k]
-                        gb[k] = (own[0] if len(own) == 1 else torch.stack(own).sum(0)).to(u.dtype)
-            gA = [g.to(a.dtype) for g, a in zip(dA, A_)]
-            gB = [g.to(b.dtype) for g, b in zip(dB, B_)]
-            return (dX, None, dY if ctx.needs_input_grad[2] else None, *gA, *gB, *gb)
-
     if W.requires_grad:
         raise ValueError("packed_lora: the base weight W is frozen; pass W with requires_grad=False")
-    return _PackedLoRAFn.apply(X, W, residual, *A, *B, *uniq)
+    call = _Call(engine, off, scales, n, plain, where, activation)
+    return _packed_lora_fn().apply(call, X, W, residual, *A, *B, *uniq)

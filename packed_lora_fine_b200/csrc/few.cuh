@@ -4,7 +4,9 @@
 //
 // Bound by the one reading of W (and of A_i and B_i), so two streaming kernels take the place of the 256-row
 // tensor-core tiles, of which a few tokens would fill a small part and a layer's columns too few blocks: for
-// 3584 x 3584 14 blocks, which read W at 0.5 TB/s.
+// 3584 x 3584 14 blocks, which read W at 0.5 TB/s.  Eight tokens of eight adapters of rank 32: 9.9 us (the
+// bytes' floor 4.5; 76 through the training kernels), 14336 x 4096, rank 64: 29 (21; 240).  At 32 tokens 20 us
+// against 76, and 62 against 240; past that the tiles fill up and their kernels take over.
 //
 // A block computes 16 rows of the streamed matrix (W's, or A_i's) times the tokens.  Its eight warps take the 64-
 // element slices of K in turn; a lane reads 16 consecutive bytes of a row, two rows and two halves of a slice at a
@@ -54,40 +56,62 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t
 }
 
 // sums[warp][16 rows][8 NT tokens] = this warp's share of (`rows` <= 16 rows at M) x (`tokens` rows at X), K each.
+// Up to eight tokens the next slices' loads are requested before a slice's products (14336 x 4096, one token: 24 us
+// against 44 without); for more the tokens' own loads, from L2, are the larger part (32 rows per block, which halves
+// them, took 16.7 us for 12.4 at 3584 x 3584, 16 tokens, and 71 for 80 at 4096 x 14336, 32 tokens: not kept).
 template <int NT>
 __device__ __forceinline__ void few_product(const __nv_bfloat16* M, int rows, const __nv_bfloat16* X, int tokens, int64_t K,
                                             float* sums) {
-    constexpr int U = NT == 4 ? 2 : 4;                 // slices in flight per warp: 64 or 32 bytes x 2 rows per lane
+    constexpr int U = 2, BUFS = NT == 1 ? 2 : 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2;
-    const bool ok0 = g < rows, ok1 = g + 8 < rows;
-    const __nv_bfloat16* const m0 = M + (ok0 ? g : 0) * K;
-    const __nv_bfloat16* const m1 = M + (ok1 ? g + 8 : 0) * K;
     const uint4 zero = make_uint4(0, 0, 0, 0);
+    const int64_t step = 8 * 64 * U, kl = (lane & 3) * 8;
     float acc[NT][4] = {};
-    for (int64_t k0 = warp * 64 + (lane & 3) * 8; k0 - (lane & 3) * 8 < K; k0 += 8 * 64 * U) {
-        uint4 a[U][2][2], x[U][NT][2];
+    uint4 a[BUFS][U][2][2], x[BUFS][U][2][NT];
+    auto fetch = [&](int64_t k0, int buf) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int64_t k = k0 + u * 512 + h * 32;
+                const int64_t k = k0 + kl + u * 512 + h * 32;
                 const bool in = k < K;
-                a[u][h][0] = in && ok0 ? __ldg(reinterpret_cast<const uint4*>(m0 + k)) : zero;
-                a[u][h][1] = in && ok1 ? __ldg(reinterpret_cast<const uint4*>(m1 + k)) : zero;
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    a[buf][u][h][r] = in && 8 * r + g < rows ? __ldg(reinterpret_cast<const uint4*>(M + (8 * r + g) * K + k)) : zero;
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
-                    x[u][t][h] = in && 8 * t + g < tokens ? __ldg(reinterpret_cast<const uint4*>(X + (8 * t + g) * K + k)) : zero;
+                    x[buf][u][h][t] = in && 8 * t + g < tokens ? __ldg(reinterpret_cast<const uint4*>(X + (8 * t + g) * K + k)) : zero;
             }
+    };
+    auto multiply = [&](int buf) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    const uint4 &p = a[u][h][0], &q = a[u][h][1], &y = x[u][t][h];
+                    const uint4 &p = a[buf][u][h][0], &q = a[buf][u][h][1], &y = x[buf][u][h][t];
                     mma_16x8x16(acc[t], p.x, q.x, p.y, q.y, y.x, y.y);
                     mma_16x8x16(acc[t], p.z, q.z, p.w, q.w, y.z, y.w);
                 }
+    };
+    int64_t k0 = warp * 64;
+    if constexpr (BUFS == 2) {
+        fetch(k0, 0);
+        while (k0 < K) {
+            fetch(k0 + step, 1);
+            multiply(0);
+            k0 += step;
+            if (k0 >= K) break;
+            fetch(k0 + step, 0);
+            multiply(1);
+            k0 += step;
+        }
+    } else {
+        for (; k0 < K; k0 += step) {
+            fetch(k0, 0);
+            multiply(0);
+        }
     }
     float* const mine = sums + warp * (kFewRows * 8 * NT);
 #pragma unroll
