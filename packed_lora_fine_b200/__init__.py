@@ -16,7 +16,7 @@ from __future__ import annotations
 import collections
 import ctypes
 import functools
-import math
+import itertools
 import os
 from typing import Iterable, List, Optional, Sequence
 
@@ -619,10 +619,8 @@ class PackedLoRA:
         return Y, saved if want_Z else None, Z
 
     def backward_epilogue(self, X, W, dY, off, scales, A, B, saved, Z=None, activation="none", want_dX=True,
-                          want_dbias=False, stream=None, dA=None, dB=None, dbias=None):
-        """The backward of ``forward_epilogue``: returns (dX, dA, dB, dbias).  dX is None without want_dX; dA and dB
-        may be given together, and dbias in place of want_dbias: lists of 16-byte aligned contiguous fp32 tensors of A's,
-        B's and the biases' shapes (dbias: or None for an adapter).
+                          want_dbias=False, stream=None):
+        """The backward of ``forward_epilogue``: returns (dX, dA, dB, dbias).  dX is None without want_dX;
         dbias is a list of fp32 ``[d_out]`` tensors, one per adapter, or None; want_dbias may be a list of
         truth values, one per adapter (dbias[i] is then None where it is false).  The residual's gradient
         is dY."""
@@ -631,21 +629,28 @@ class PackedLoRA:
         self._check_tensors(X.shape[0], X=X, W=W, dY=dY, Z=Z)
         self._check_factors(A, B, n)
         f32 = dict(dtype=torch.float32, device=X.device)
-        if dA is None and dB is None:
-            dA, dB = [torch.empty(a.shape, **f32) for a in A], [torch.empty(b.shape, **f32) for b in B]
-        dX = torch.empty_like(X) if want_dX else None
+        dA, dB = [torch.empty(a.shape, **f32) for a in A], [torch.empty(b.shape, **f32) for b in B]
         want = list(want_dbias) if isinstance(want_dbias, (list, tuple)) else [bool(want_dbias)] * n
-        db = dbias if dbias is not None else [torch.empty(self.d_out, **f32) if w else None for w in want] if any(want) else None
-        tab = self.table(scales, A, B, dA, dB)
-        ep = make_epilogue(activation, dbias=None if db is None else [b.data_ptr() if b is not None else None for b in db],
-                           Z=Z.data_ptr() if Z is not None else None)
+        db = [torch.empty(self.d_out, **f32) if w else None for w in want] if any(want) else None
+        dX = self._gradients(X, W, dY, off, scales, A, B, saved, Z, activation, want_dX, [g.data_ptr() for g in dA],
+                             [g.data_ptr() for g in dB],
+                             None if db is None else [b.data_ptr() if b is not None else None for b in db], stream)
+        return dX, dA, dB, db
+
+    def _gradients(self, X, W, dY, off, scales, A, B, saved, Z, activation, want_dX, pA, pB, pb, stream=None):
+        """backward_epilogue into the fp32 buffers at the device pointers pA, pB and pb; returns dX."""
+        import torch
+        n = len(off) - 1
+        dX = torch.empty_like(X) if want_dX else None
+        tab = make_table([b.shape[1] for b in B], scales, [a.data_ptr() for a in A], [b.data_ptr() for b in B], pA, pB)
+        ep = make_epilogue(activation, dbias=pb, Z=Z.data_ptr() if Z is not None else None)
         nbytes = plora_epilogue_work_bytes(self.h, n, off, ep)
         work = torch.empty(nbytes, dtype=torch.uint8, device=X.device) if nbytes else None
         ep.work = work.data_ptr() if work is not None else None
         st = (stream or torch.cuda.current_stream(X.device)).cuda_stream
         plora_backward_epilogue(self.h, X.data_ptr(), W.data_ptr(), dY.data_ptr(), dX.data_ptr() if want_dX else None,
                                 n, off, tab, saved.data_ptr(), ep, st)
-        return dX, dA, dB, db
+        return dX
 
 
 # ---------------------------------------------------------------- layer calls
@@ -803,31 +808,31 @@ def _packed_lora_fn():
             need_b = ctx.needs_input_grad[4 + 2 * n:]
             want_dX = ctx.needs_input_grad[1]
             gb = [None] * len(need_b)
-            # the fp32 gradients lie in one buffer, so that one launch casts them
-            want_db = [k is not None and need_b[k] for k in call.where]
-            shapes = [t.shape for t in AB] + [(dY.shape[1],)] * sum(want_db)
-            counts = [math.prod(s) for s in shapes]
-            sizes = [-(-c // 64) * 64 for c in counts]
-
-            def cut(buf):
-                return [g[:c].view(s) for g, c, s in zip(buf.split(sizes), counts, shapes)] if sizes else []
-            flat = torch.empty(sum(sizes), dtype=torch.float32, device=dY.device)
-            g32 = cut(flat)
-            grads = dict(dA=g32[:n], dB=g32[n:2 * n], want_dX=want_dX)
+            # The fp32 gradients lie in one buffer, so that one launch casts them (d_in and d_out are multiples of 8,
+            # so that each starts on 32 bytes).
+            owners = [i for i, k in enumerate(call.where) if k is not None and need_b[k]]
+            counts = [t.numel() for t in AB] + [dY.shape[1]] * len(owners)
+            flat = torch.empty(sum(counts), dtype=torch.float32, device=dY.device)
+            ptrs = list(itertools.accumulate(counts, lambda at, c: at + 4 * c, initial=flat.data_ptr()))
             if call.plain:
-                dX, _, _ = call.engine.backward(X_, W_, dY.contiguous(), call.off, call.scales, A_, B_, saved, **grads)
+                dX = torch.empty_like(X_) if want_dX else None
+                tab = make_table([b.shape[1] for b in B_], call.scales, [a.data_ptr() for a in A_], [b.data_ptr() for b in B_],
+                                 ptrs[:n], ptrs[n:2 * n])
+                plora_backward(call.engine.h, X_.data_ptr(), W_.data_ptr(), dY.contiguous().data_ptr(),
+                               dX.data_ptr() if want_dX else None, n, call.off, tab, saved.data_ptr(),
+                               torch.cuda.current_stream().cuda_stream)
             else:
-                rest = iter(g32[2 * n:])
-                dX, _, _, _ = call.engine.backward_epilogue(X_, W_, dY.contiguous(), call.off, call.scales, A_, B_, saved, Z=Z,
-                                                            activation=call.activation, **grads,
-                                                            dbias=[next(rest) if w else None for w in want_db]
-                                                            if any(want_db) else None)
-            g = cut(flat.to(dY.dtype)) if dY.dtype != flat.dtype else g32
+                pb = [None] * n
+                for i, at in zip(owners, ptrs[2 * n:]):
+                    pb[i] = at
+                dX = call.engine._gradients(X_, W_, dY.contiguous(), call.off, call.scales, A_, B_, saved, Z, call.activation,
+                                            want_dX, ptrs[:n], ptrs[n:2 * n], pb if owners else None)
+            g = list((flat if flat.dtype == dY.dtype else flat.to(dY.dtype)).split(counts)) if counts else []
             for k, need in enumerate(need_b):       # a shared bias sums its adapters' fp32 gradients
                 if need:
-                    own = [2 * n + sum(want_db[:i]) for i in range(n) if call.where[i] == k]
-                    gb[k] = g[own[0]] if len(own) == 1 else torch.stack([g32[j] for j in own]).sum(0).to(dY.dtype)
-            g = g[:2 * n]
+                    own = [2 * n + j for j, i in enumerate(owners) if call.where[i] == k]
+                    gb[k] = g[own[0]] if len(own) == 1 else torch.stack([flat.split(counts)[j] for j in own]).sum(0).to(dY.dtype)
+            g = [x.view(t.shape) for x, t in zip(g, AB)]
             return (None, dX, None, dY if ctx.needs_input_grad[3] else None, *g, *gb)
 
     return PackedLoRAFn
