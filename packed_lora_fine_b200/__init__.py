@@ -208,10 +208,9 @@ def make_table(ranks: Sequence[int], scales: Sequence[float], A: Sequence[int], 
                dA: Optional[Sequence[int]] = None, dB: Optional[Sequence[int]] = None):
     """Build a host plora_adapter[] from ranks, scales and device pointers (ints)."""
     n = len(ranks)
-    none = (None,) * n
     return (plora_adapter * max(1, n))(*[
-        (int(r), float(s), int(a), int(b), None if da is None else int(da), None if db is None else int(db))
-        for r, s, a, b, da, db in zip(ranks, scales, A, B, none if dA is None else dA, none if dB is None else dB)])
+        (int(ranks[i]), float(scales[i]), int(A[i]), int(B[i]), None if dA is None else int(dA[i]),
+         None if dB is None else int(dB[i])) for i in range(n)])
 
 
 # ---------------------------------------------------------------- C names
@@ -616,6 +615,8 @@ class PackedLoRA:
                            Z=Z.data_ptr() if Z is not None else None, inference=not want_Z)
         st = (stream or torch.cuda.current_stream(X.device)).cuda_stream
         plora_forward_epilogue(self.h, X.data_ptr(), W.data_ptr(), Y.data_ptr(), n, off, tab, saved.data_ptr(), ep, st)
+        if not want_Z and stream is not None:     # scratch that goes back to the allocator while the stream may use it
+            saved.record_stream(stream)
         return Y, saved if want_Z else None, Z
 
     def backward_epilogue(self, X, W, dY, off, scales, A, B, saved, Z=None, activation="none", want_dX=True,
@@ -650,6 +651,8 @@ class PackedLoRA:
         st = (stream or torch.cuda.current_stream(X.device)).cuda_stream
         plora_backward_epilogue(self.h, X.data_ptr(), W.data_ptr(), dY.data_ptr(), dX.data_ptr() if want_dX else None,
                                 n, off, tab, saved.data_ptr(), ep, st)
+        if work is not None and stream is not None:
+            work.record_stream(stream)
         return dX
 
 

@@ -395,10 +395,13 @@ static_assert(kGramSmem + 1024 <= 232448, "shared memory per CTA");
 constexpr int kGramExactTiles = 16;     // tiles whose x0 x0 sums stay below 2^24 (|x0| <= 128, 64 columns each)
 
 // One item: the partial Gram matrix (of its two equal halves the elements [c][r], c <= r) of a run of tiles
-// over one pair of 64-row groups (the only pair for s <= 128).  Sixteen warps copy a tile's g and m to shared memory (two tiles ahead, every thread
-// its own elements) and split u into one of two places; a further warp issues a place's products.
+// over one pair of 64-row groups (the only pair for s <= 128).  Sixteen warps copy a tile's g and m to shared memory
+// (two tiles ahead, every thread its own elements) and split u into one of two places; a further warp issues a place's products.
 // The scale of the split is a power of two, 1.5 to 3 times the first tile's largest |u|.  A tile that exceeds it
 // takes the sums out of the accumulators and starts them anew at its own scale, and so does every 16th tile.
+// 8 bytes per element: 32 adapters of rank 8 to 128 at 4096 -> 14336 (40 M elements) take 183 us for the bytes' 49, 3.6
+// us per tile (1.1 of them the products') and 8 per item to begin and to take the sums out; what bounds a tile is the
+// chain from its copies through the split and the proxy fence to its products, one tile at a time over the block.
 __global__ void __launch_bounds__(kGramThreads, 1)
 muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_t timeout_ns) {
     extern __shared__ uint8_t raw[];
@@ -408,10 +411,13 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ volatile int what[2];
+    __shared__ int which;
     __shared__ float red[kGramLoad / 32];
     __shared__ MuonMat record;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    muon_fetch(&record, mats + muon_find(0, n - 1, blockIdx.x, [&](int k) { return mats[k].gram0; }));
+    // the item's matrix, found by all threads at once (a search would wait for six loads in turn)
+    for (int k = tid; k < n; k += kGramThreads)
+        if (mats[k].gram0 <= (int)blockIdx.x && (k + 1 == n || mats[k + 1].gram0 > (int)blockIdx.x)) which = k;
     if (tid == 0) {
         for (int k = 0; k < 2; ++k) {
             ptx::mbar_init(&full[k], kGramLoad / 32);
@@ -430,6 +436,8 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
+    muon_fetch(&record, mats + which);
+    __syncthreads();
     const MuonMat& M = record;
     const int item = blockIdx.x - M.gram0;
     const int chunk = item / M.npairs;
@@ -664,6 +672,11 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
 //              stages; a block computes the blocks of its rows on and after the diagonal, half of them, cyclically,
 //              and writes them to both places.
 // (Products of symmetric matrices that commute are symmetric: B's rows serve as its columns.)
+// Five steps, with the sum of the partials: one matrix of 16 27 us, of 64 64, of 128 137, of 256 427; 64 of 8 to 128
+// (ranks of 32 adapters) 186; sixteen of 256 612.  Bound by the fp64 pipe and, as much again, by the short products'
+// barriers and loads: a step at 128 takes 25 us, 17 of them the pipe's, at 256 90 of which 43.  Clusters of eight with
+// 16 rows each were faster for one matrix of 128 (92 us) but with their 186 KB only 15 are resident at once, and the
+// up mix took 274; products dealt over eight blocks from L2, with two barriers more per step, 218 and 890.
 constexpr int kNsRows = 32;                            // rows of a cluster's block
 constexpr int kNsPitch = 64 + 4;                       // doubles; rows shift by 4 so that fragment loads spread
 constexpr int kNsSmallS = 64;
@@ -1160,6 +1173,9 @@ static_assert(kApplySmem + 1024 <= 232448, "shared memory per CTA");
 //            accumulators, of two such sets in turn
 //   finish   p to shared memory (two blocks ahead), O out of the accumulators onto it, the new p and its copy
 // BIG (s > 128): tiles of 256 rows in one place, Q's (row half, column block) pieces streamed from L2.
+// 22 bytes per element: 32 adapters of rank 8 to 128 at 4096 -> 14336 (40 M elements) take 268 us for the bytes' 134,
+// 4096 x 128 matrices alone (67 M) 336 for 225; odd short sides cost most (their rows start off 16 bytes).  BIG: 146
+// for 56.  Bound by the loading warps' work per element, loads and splits in turn, not by the products.
 template <bool BIG>
 __global__ void __launch_bounds__(kApplyThreads, 1)
 muon_apply_kernel(const MuonMat* __restrict__ mats, int first, int last, int tiles, int* err_flag, uint64_t timeout_ns) {

@@ -671,6 +671,8 @@ __device__ __forceinline__ const __nv_bfloat16* bias_of_row(const TcParams& p, c
 // applied to the fp32 accumulator, so Y and Z are each rounded once.  A lane owns one output row: its
 // bias loads hit the same line in every lane whose row has the same adapter, and its residual loads
 // (requested before the accumulator is read) take whole 128-byte lines over a 64-column chunk.
+// 16384 x 4096 -> 14336 with silu: 1415 us, what the products alone take; 1610 with Z written too (470 MB more and
+// twice the staging).  With CUDA's accurate functions, whose divisions branch, the four warps took 1877 and 2160.
 __device__ __forceinline__ void epilogue_store_ep(const CUtensorMap* tmY, const CUtensorMap* tmZ, uint32_t t_row,
                                                   uint8_t* wbuf, int lane, int row0, int n0, int M_total, int N_total,
                                                   const EpiFused& ep, const __nv_bfloat16* bias, uint32_t& seq) {

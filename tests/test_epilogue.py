@@ -498,6 +498,24 @@ def test_few_tokens_alone_in_place_and_captured():
     assert torch.equal(R[:p.T], Y) and torch.equal(R[p.T:], p.R[p.T:])
     out, saved = torch.empty_like(Y), torch.empty(eng.saved_bytes(p.off, eng.table(p.scales, p.A, p.B)), dtype=torch.uint8,
                                                   device="cuda")
+    bad = p.X.clone()                  # a token's NaN and infinity stay in its row
+    bad[9] = math.nan
+    bad[10, 3] = math.inf
+    keep, p.X = p.X, bad
+    got = infer(p, eng, "silu")
+    p.X = keep
+    rows = [t for t in range(p.T) if t not in (9, 10)]
+    assert torch.equal(got[rows], Y[rows]) and bool(got[9].isnan().all()) and not bool(got[10].isfinite().any())
+    side = torch.cuda.Stream()         # another stream than the current one, behind work of its own
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        x = p.X * 2
+    y, _, _ = eng.forward_epilogue(x, p.W, p.off, p.scales, p.A, p.B, bias=p.bias, activation="silu", residual=p.R, want_Z=False,
+                                   stream=side)
+    keep, p.X = p.X, p.X * 2
+    torch.cuda.synchronize()
+    assert torch.equal(y[:p.T], infer(p, eng, "silu"))
+    p.X = keep
     graph = torch.cuda.CUDAGraph()     # no schedule slot is reserved
     torch.cuda.synchronize()
     with torch.cuda.graph(graph):
