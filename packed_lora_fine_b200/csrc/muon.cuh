@@ -672,17 +672,18 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
 //              stages; a block computes the blocks of its rows on and after the diagonal, half of them, cyclically,
 //              and writes them to both places.
 // (Products of symmetric matrices that commute are symmetric: B's rows serve as its columns.)
-// Five steps, with the sum of the partials: one matrix of 16 27 us, of 64 64, of 128 137, of 256 427; 64 of 8 to 128
-// (ranks of 32 adapters) 186; sixteen of 256 612.  Bound by the fp64 pipe and, as much again, by the short products'
-// barriers and loads: a step at 128 takes 25 us, 17 of them the pipe's, at 256 90 of which 43.  Clusters of eight with
-// 16 rows each were faster for one matrix of 128 (92 us) but with their 186 KB only 15 are resident at once, and the
-// up mix took 274; products dealt over eight blocks from L2, with two barriers more per step, 218 and 890.
+// Five steps, with the sum of the partials: one matrix of 16 27 us, of 64 64, of 128 137, of 256 357; 64 of 8 to 128
+// (ranks of 32 adapters) 186; fifteen of 256 366, sixteen 546 (15 clusters of eight have an SM per block; two blocks of
+// an SM share its pipe).  Bound by the fp64 pipe and, nearly as much again, by the short products' barriers and loads:
+// a step at 128 takes 25 us, 17 of them the pipe's, at 256 73 of which 43.  Clusters of eight with 16 rows each were
+// faster for one matrix of 128 (92 us) but with their 186 KB only 15 are resident at once, and the up mix took 274;
+// products dealt over eight blocks from L2, with two barriers more per step, 218 and (sixteen of 256) 890.
 constexpr int kNsRows = 32;                            // rows of a cluster's block
 constexpr int kNsPitch = 64 + 4;                       // doubles; rows shift by 4 so that fragment loads spread
 constexpr int kNsSmallS = 64;
 constexpr int kNsMidS = 128, kNsMidPitch = kNsMidS + 4, kNsMidCluster = kNsMidS / kNsRows;
 constexpr int kNsBigPitch = 256 + 4, kNsBigCluster = 256 / kNsRows;
-constexpr int kNsK = 32, kNsStages = 4, kNsStage = kNsRows * (kNsK + 4);   // doubles of one stage of the streamed operand
+constexpr int kNsK = 64, kNsStages = 2, kNsStage = kNsRows * (kNsK + 4);   // doubles of one stage of the streamed operand
 constexpr int kNsSmallSmem = 3 * kNsSmallS * kNsPitch * 8;
 constexpr int kNsMidSmem = (kNsMidS + 2 * kNsRows) * kNsMidPitch * 8;
 constexpr int kNsBigSmem = (kNsRows * kNsBigPitch + kNsStages * kNsStage) * 8;
@@ -864,6 +865,10 @@ muon_ns_kernel(const MuonMat* __restrict__ mats, const int32_t* __restrict__ ord
     const MuonMat& M = record;
     const int rank = small ? 0 : (int)ptx::cluster_ctarank();
     const int tid = threadIdx.x, warp = tid >> 5, s = M.s, sp = (s + 7) & ~7, k8 = sp / 8;
+    // Blocks past the matrix's rows leave: the cluster's barrier waits for threads that have not ended, and nobody
+    // copies or stores into theirs.  (Sixteen matrices of 200: 403 us, 435 with them in every barrier.)
+    const int active = small ? 1 : (s + kNsRows - 1) / kNsRows;
+    if (rank >= active) return;
     // this block's rows of G and Q (from row r0 of the matrix on), and its own copies' pitch
     const int nr = small ? s : kNsRows, r0 = rank * kNsRows;
     const int pitch = BIG ? kNsBigPitch : small ? kNsPitch : kNsMidPitch;
@@ -924,8 +929,7 @@ muon_ns_kernel(const MuonMat* __restrict__ mats, const int32_t* __restrict__ ord
         double* gG = M.ns;
         double *gP = gG + sp * sp, *gQ = gP + sp * sp, *gR = gQ + sp * sp, *gS = gR + sp * sp;
         double* const stages = sm + kNsRows * kNsBigPitch;
-        const int n = (s + kNsRows - 1) / kNsRows;        // blocks of 32 rows, and of 32 columns
-        const bool work = rank < n;
+        const int n = active;                             // blocks of 32 rows, and of 32 columns
         // rows of `X` for the left operand
         auto rows_of = [&](const double* X) {
             __syncthreads();
@@ -938,37 +942,57 @@ muon_ns_kernel(const MuonMat* __restrict__ mats, const int32_t* __restrict__ ord
         };
         // C = f(those rows times X): the blocks (rank, rank + d mod n), 32 x 32 each, a warp's share 16 x 8
         const int wr = (warp & 1) * 16, wc = (warp >> 1) * 8;
+        const int lane = tid & 31;
+        const double* const as0 = G + (wr + (lane >> 2)) * kNsBigPitch + (lane & 3);
+        const double* const bs0 = stages + (wc + (lane >> 2)) * (kNsK + 4) + (lane & 3);
         auto product = [&](const double* X, double* C, auto&& f) {
             const int nk = (sp + kNsK - 1) / kNsK, steps = (n / 2 + 1) * nk;
-            const int fr = tid >> 4, fc = (tid & 15) * 2;      // this thread's pieces of a stage: rows fr, fr + 16
-            int fd = 0, fk = 0, ck = 0, cd = 0;
+            const int fr = tid >> 5, fc = lane * 2;            // this thread's pieces of a stage: rows fr + 8 i
+            const uint32_t dst0 = ptx::smem_u32(stages + fr * (kNsK + 4) + fc);
+            int fd = 0, fk = 0, ck = 0, cd = 0, rows = 0;
+            const double* src = X;
             auto fetch = [&](int k) {
                 if (k < steps) {
-                    int col = rank + fd;
-                    if (col >= n) col -= n;
-                    const uint32_t dst = ptx::smem_u32(stages + (k % kNsStages) * kNsStage + fr * (kNsK + 4) + fc);
-                    const int k0 = fk * kNsK + fc;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = col * kNsRows + fr + 16 * i;
-                        const bool ok = r < sp && k0 < sp;
-                        ptx::cp_async16(dst + 16 * i * (kNsK + 4) * 8, ok ? X + r * sp + k0 : X, ok ? 16 : 0);
+                    if (fk == 0) {
+                        int col = rank + fd;
+                        if (col >= n) col -= n;
+                        rows = sp - (col * kNsRows + fr);
+                        src = X + (col * kNsRows + fr) * sp + fc;
                     }
+                    const uint32_t dst = dst0 + (k & 1) * kNsStage * 8;
+                    const bool in = fk * kNsK + fc < sp;
+#pragma unroll
+                    for (int i = 0; i < kNsRows / 8; ++i) {
+                        const bool ok = in && 8 * i < rows;
+                        ptx::cp_async16(dst + 8 * i * (kNsK + 4) * 8, ok ? src + 8 * i * sp : X, ok ? 16 : 0);
+                    }
+                    src += kNsK;
                     if (++fk == nk) { fk = 0; ++fd; }
                 }
                 ptx::cp_async_commit();
             };
             double acc[2][1][1][4] = {};          // even and odd steps of eight: two chains of products
-            for (int k = 0; k < kNsStages - 1; ++k) fetch(k);
+            fetch(0);
             for (int k = 0; k < steps; ++k) {
-                ptx::cp_async_wait<kNsStages - 2>();
-                __syncthreads();                  // the stage is there, and every warp has left the one fetched next
-                fetch(k + kNsStages - 1);
-                const double* const as = G + wr * kNsBigPitch + ck * kNsK;
-                const double* const bs = stages + (k % kNsStages) * kNsStage + wc * (kNsK + 4);
+                ptx::cp_async_wait<0>();
+                __syncthreads();                  // the stage is there, and every warp has left the other one
+                fetch(k + 1);
+                const double* const as = as0 + ck * kNsK;
+                const double* const bs = bs0 + (k & 1) * kNsStage;
+                auto multiply = [&](int q) {
+                    const double x[4] = {as[8 * q], as[8 * q + 8 * kNsBigPitch], as[8 * q + 4], as[8 * q + 8 * kNsBigPitch + 4]};
+                    const double y[2] = {bs[8 * q], bs[8 * q + 4]};
+                    dmma_16x8x8(acc[q & 1][0][0], x, y);
+                };
+                const int kn = k8 - ck * (kNsK / 8);
+                if (kn >= kNsK / 8) {
 #pragma unroll
-                for (int q = 0; q < kNsK / 8; ++q)
-                    if (ck * (kNsK / 8) + q < k8) dmma_block(acc[q & 1], as + 8 * q, kNsBigPitch, bs + 8 * q, kNsK + 4, 1);
+                    for (int q = 0; q < kNsK / 8; ++q) multiply(q);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kNsK / 8; ++q)
+                        if (q < kn) multiply(q);
+                }
                 if (++ck < nk) continue;
                 int col = rank + cd;
                 if (col >= n) col -= n;
@@ -999,20 +1023,18 @@ muon_ns_kernel(const MuonMat* __restrict__ mats, const int32_t* __restrict__ ord
         for (int k = 0; k < M.steps; ++k) {
             const bool last = k + 1 == M.steps;
             double* const P = k == 0 ? gQ : gP;   // (the first step's P is Q_1)
-            if (work) {
-                if (k > 0) rows_of(gG);
-                product(gG, P, [&](int i, int j, double v) {
-                    return (i == j && i < s ? a : 0.0) + b * G[(i - r0) * kNsBigPitch + j] + c * v;
-                });
-            }
+            if (k > 0) rows_of(gG);
+            product(gG, P, [&](int i, int j, double v) {
+                return (i == j && i < s ? a : 0.0) + b * G[(i - r0) * kNsBigPitch + j] + c * v;
+            });
             sync();
-            if (work && !last) product(P, gR, plain);
-            if (work && k > 0) {
+            if (!last) product(P, gR, plain);
+            if (k > 0) {
                 rows_of(gQ);
                 product(P, gS, plain);
             }
             if (k + 1 < M.steps || k > 0) sync();
-            if (work && !last) {
+            if (!last) {
                 rows_of(gR);
                 product(P, gG, plain);
             }
@@ -1024,10 +1046,8 @@ muon_ns_kernel(const MuonMat* __restrict__ mats, const int32_t* __restrict__ ord
             if (last) break;
             sync();
         }
-        if (work) {
-            rows_of(gQ);
-            ptx::cp_async_wait<0>();
-        }
+        rows_of(gQ);
+        ptx::cp_async_wait<0>();
         __syncthreads();
     } else if (small) {
         double* const P = G + kNsSmallS * kNsPitch;
@@ -1049,16 +1069,14 @@ muon_ns_kernel(const MuonMat* __restrict__ mats, const int32_t* __restrict__ ord
         }
     } else {
         const int c0 = warp * 16;                 // this warp's columns
-        const bool work = r0 < s && c0 < s;
-        // The blocks that have rows send theirs, as they lie in their own copy, to each other's.
-        const int active = (s + kNsRows - 1) / kNsRows;
+        const bool work = c0 < s;
+        // The blocks send their rows, as they lie in their own copy, to each other's.
         constexpr uint32_t kRowsBytes = kNsRows * kNsMidPitch * 8;
         constexpr int p = kNsMidPitch;
         double* const F = sm;
         double* const own = F + r0 * p;
         uint32_t parity = 0;
         auto exchange = [&]() {
-            if (rank >= active) return;
             ptx::fence_proxy_async_smem();
             __syncthreads();
             if (tid == 0) {
@@ -1118,10 +1136,10 @@ muon_ns_kernel(const MuonMat* __restrict__ mats, const int32_t* __restrict__ ord
         if (r0 + e / s < s) qmax = ptx::max_nan(qmax, (float)fabs(Q[(e / s) * pitch + e % s]));
     qmax = block_max(qmax);
     if (!small) {
-        if (tid < CLUSTER) ptx::st_cluster_f32(ptx::cluster_addr(&qmaxes[rank], tid), qmax);
+        if (tid < active) ptx::st_cluster_f32(ptx::cluster_addr(&qmaxes[rank], tid), qmax);
         sync();
         qmax = 0.f;
-        for (int k = 0; k < CLUSTER; ++k) qmax = ptx::max_nan(qmax, qmaxes[k]);
+        for (int k = 0; k < active; ++k) qmax = ptx::max_nan(qmax, qmaxes[k]);
         // (no block ends while another stores into it: all have, before the barrier)
     }
     const int eq = qmax > 0.f && qmax < 3e38f ? ilogbf(qmax) + 1 : 0, eu = max(umax > 0.f ? ilogbf(umax) + 1 : -100, -100);
@@ -1132,9 +1150,9 @@ muon_ns_kernel(const MuonMat* __restrict__ mats, const int32_t* __restrict__ ord
         const bool fine = tr * 0.0 == 0.0 && qmax < 3e38f;
         M.hdr[1] = fine ? (float)(inv * scalbn(1.0, eu - 8 + eq - 8)) : __int_as_float(0x7fc00000);
     }
-    // the parts of this block's rows of the 128 (or 256) that the apply pass takes
+    // the parts of this block's rows of the 128 (or 256) that the apply pass takes; the last block's go to the end
     constexpr int w = BIG ? 256 : 128, kblocks = w / 64;
-    const int rows = small ? w : nr;
+    const int rows = small ? w : rank + 1 < active ? nr : w - r0;
     for (int e = tid; e < rows * (w / 8); e += 256) {
         const int r = e / (w / 8), k8i = e - r * (w / 8), row = r0 + r;
         const int jr = row / s, cr = row - jr * s;
@@ -1142,7 +1160,7 @@ muon_ns_kernel(const MuonMat* __restrict__ mats, const int32_t* __restrict__ ord
         __align__(16) __half h[3][8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const double v = jr < M.J && jr == jk ? Q[(small ? cr : r) * pitch + ck] * qs : 0.0;
+            const double v = jr < M.J && jr == jk ? Q[(small ? cr : r) * pitch + ck] * qs : 0.0;   // (row < s)
             const double x0 = rint(v);
             h[0][k] = __double2half(x0);
             h[1][k] = __double2half(v - x0);
