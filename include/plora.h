@@ -238,7 +238,7 @@ typedef enum {
  * ignores dbias and work, the backward bias and residual (dR is dY).  Every other pointer is 16-byte
  * aligned.  A buffer that a call writes must not overlap another of these buffers, Y, dY or dX
  * (PLORA_ERR_INVALID_ARG), except residual = Y.
- * inference 1: a forward without a backward.  Z is NULL, and `saved`, of plora_saved_bytes() as ever, is scratch
+ * inference 1: a forward without a backward.  Z is NULL, and `saved`, of plora_saved_bytes(), is scratch
  * that holds nothing afterwards.  With a bf16 handle and at most 32 tokens such a call reads W once in kernels for
  * few tokens, takes no schedule slot (a capture needs none reserved for it) and sums in another order than a
  * training call; a token's result does not depend on the call's other tokens within 32, or above.
@@ -256,6 +256,11 @@ typedef struct {
 /* Size of the backward's scratch for this segment map, activation and set of wanted dbias entries. */
 PLORA_API plora_status plora_epilogue_work_bytes(plora_handle h, int32_t n_adapters, const int64_t* off,
                                                  const plora_epilogue* ep, size_t* bytes);
+/* Size of `saved` for a forward with this epilogue: plora_saved_bytes(), but more for relu with Z on a bf16 handle,
+ * whose forward then takes H' in two bf16 parts (relu's derivative jumps with Z's sign).  Of ep, activation and
+ * whether Z is NULL are read.  The backward reads the first plora_saved_bytes() of it. */
+PLORA_API plora_status plora_epilogue_saved_bytes(plora_handle h, int32_t n_adapters, const int64_t* off,
+                                                  const plora_adapter* tab, const plora_epilogue* ep, size_t* bytes);
 /* plora_forward with an epilogue (not NULL).  Other arguments, errors and captures as for plora_forward. */
 PLORA_API plora_status plora_forward_epilogue(plora_handle h, const void* X, const void* W, void* Y,
                                               int32_t n_adapters, const int64_t* off, const plora_adapter* tab,

@@ -156,11 +156,12 @@ def load(path: str = LIB_PATH):
     lib.plora_adamw_step.argtypes = [H, I32, P, P, P]
     lib.plora_adamw_step.restype = ctypes.c_int
     lib.plora_epilogue_work_bytes.argtypes = [H, I32, P, P, ctypes.POINTER(ctypes.c_size_t)]
+    lib.plora_epilogue_saved_bytes.argtypes = [H, I32, P, P, P, ctypes.POINTER(ctypes.c_size_t)]
     lib.plora_forward_epilogue.argtypes = [H, P, P, P, I32, P, P, P, P, P]
     lib.plora_backward_epilogue.argtypes = [H, P, P, P, P, I32, P, P, P, P, P]
     lib.plora_muon_work_bytes.argtypes = [H, I32, P, ctypes.POINTER(ctypes.c_size_t)]
     lib.plora_muon_step.argtypes = [H, I32, P, P, P, P]
-    for fn in ("plora_epilogue_work_bytes", "plora_forward_epilogue", "plora_backward_epilogue",
+    for fn in ("plora_epilogue_work_bytes", "plora_epilogue_saved_bytes", "plora_forward_epilogue", "plora_backward_epilogue",
                "plora_muon_work_bytes", "plora_muon_step"):
         getattr(lib, fn).restype = ctypes.c_int
     lib.plora_grad_B_static.argtypes = [ctypes.POINTER(plora_config), P, I32, P, P, P, P]
@@ -454,6 +455,14 @@ def plora_epilogue_work_bytes(h: int, n: int, off, ep: plora_epilogue) -> int:
     return int(out.value)
 
 
+def plora_epilogue_saved_bytes(h: int, n: int, off, tab, ep: plora_epilogue) -> int:
+    off = _offsets(off)
+    out = ctypes.c_size_t(0)
+    _raise(h, load().plora_epilogue_saved_bytes(h, n, off.ctypes.data, ctypes.addressof(tab), ctypes.addressof(ep),
+                                                ctypes.byref(out)))
+    return int(out.value)
+
+
 def plora_forward_epilogue(h: int, X: int, W: int, Y: int, n: int, off, tab, saved: int, ep: plora_epilogue,
                            stream: int = 0, check: bool = True) -> int:
     off = _offsets(off)
@@ -607,12 +616,12 @@ class PackedLoRA:
         tab = self.table(scales, A, B)
         if Y is None:
             Y = torch.empty((X.shape[0], self.d_out), dtype=X.dtype, device=X.device)
-        if saved is None:
-            saved = torch.empty(max(self.saved_bytes(off, tab), 256), dtype=torch.uint8, device=X.device)
         Z = torch.empty_like(Y) if want_Z and activation != "none" else None
         ep = make_epilogue(activation, None if bias is None else [b.data_ptr() if b is not None else None for b in bias],
                            residual=residual.data_ptr() if residual is not None else None,
                            Z=Z.data_ptr() if Z is not None else None, inference=not want_Z)
+        if saved is None:
+            saved = torch.empty(max(plora_epilogue_saved_bytes(self.h, n, off, tab, ep), 256), dtype=torch.uint8, device=X.device)
         st = (stream or torch.cuda.current_stream(X.device)).cuda_stream
         plora_forward_epilogue(self.h, X.data_ptr(), W.data_ptr(), Y.data_ptr(), n, off, tab, saved.data_ptr(), ep, st)
         if not want_Z and stream is not None:     # scratch that goes back to the allocator while the stream may use it

@@ -399,8 +399,8 @@ constexpr int kGramExactTiles = 16;     // tiles whose x0 x0 sums stay below 2^2
 // (two tiles ahead, every thread its own elements) and split u into one of two places; a further warp issues a place's products.
 // The scale of the split is a power of two, 1.5 to 3 times the first tile's largest |u|.  A tile that exceeds it
 // takes the sums out of the accumulators and starts them anew at its own scale, and so does every 16th tile.
-// 8 bytes per element: 32 adapters of rank 8 to 128 at 4096 -> 14336 (40 M elements) take 183 us for the bytes' 49, 3.6
-// us per tile (1.1 of them the products') and 8 per item to begin and to take the sums out; what bounds a tile is the
+// 8 bytes per element: 32 adapters of rank 8 to 128 at 4096 -> 14336 (40 M elements) take 176 us for the bytes' 49, 3.5
+// us per tile (1.1 of them the products') and 7 per item to begin and to take the sums out; what bounds a tile is the
 // chain from its copies through the split and the proxy fence to its products, one tile at a time over the block.
 __global__ void __launch_bounds__(kGramThreads, 1)
 muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_t timeout_ns) {
@@ -1192,8 +1192,10 @@ static_assert(kApplySmem + 1024 <= 232448, "shared memory per CTA");
 //   finish   p to shared memory (two blocks ahead), O out of the accumulators onto it, the new p and its copy
 // BIG (s > 128): tiles of 256 rows in one place, Q's (row half, column block) pieces streamed from L2.
 // 22 bytes per element: 32 adapters of rank 8 to 128 at 4096 -> 14336 (40 M elements) take 268 us for the bytes' 134,
-// 4096 x 128 matrices alone (67 M) 336 for 225; odd short sides cost most (their rows start off 16 bytes).  BIG: 146
-// for 56.  Bound by the loading warps' work per element, loads and splits in turn, not by the products.
+// 65536 x 128 matrices alone (67 M) 336 for 225; odd short sides cost most (their rows start off 16 bytes).  BIG: 146
+// for 56.  Bound by the roles sharing an SM: of the 336, 209 are left without p's traffic, 182 without the stores of m
+// and the split as well, 157 without the products, and 181 with everything but the traffic.  Loads of a step ahead in
+// registers did not help (342).
 template <bool BIG>
 __global__ void __launch_bounds__(kApplyThreads, 1)
 muon_apply_kernel(const MuonMat* __restrict__ mats, int first, int last, int tiles, int* err_flag, uint64_t timeout_ns) {

@@ -424,6 +424,33 @@ SavedLayout saved_layout(const plora_ctx* h, const HostPlan& P) {
 
 size_t saved_bytes_of(const plora_ctx* h, const HostPlan& P) { return saved_layout(h, P).bytes; }
 
+// relu's derivative jumps where Z changes its sign, so a forward that keeps Z for it takes H' in two bf16 parts,
+// high and low: with H' rounded to bf16 alone, Z is off by 2^-9 of the low-rank part, and as many signs of small
+// Zs with it (10808 -> 544, rank 1 and scale 16: dX 0.0075 off in the 2-norm, 0.002 with both parts).  What is left
+// are the fp32 sums' own errors.  The low parts lie behind the packed
+// factors, in rows of the same pitch: the first of them, and the size of `saved` with them.
+bool relu_low(const plora_ctx* h, int32_t act, bool keeps_z) { return h->tc && act == PLORA_ACT_RELU && keeps_z; }
+int64_t low_row_of(const plora_ctx* h, const HostPlan& P) { return ceil_div((int64_t)saved_bytes_of(h, P), P.RP * 2); }
+size_t low_bytes_of(const plora_ctx* h, const HostPlan& P) {
+    return (size_t)(low_row_of(h, P) + P.h_rows) * (size_t)P.RP * 2;
+}
+// Folds each adapter's low parts like another adapter's rows, with the same factor.
+void fold_low_parts(HostPlan& P, int64_t low_row) {
+    std::vector<LoraSeg> seg;
+    for (MTileRec& r : P.mt_rec) {
+        const int32_t q0 = (int32_t)seg.size();
+        for (int part = 0; part < 2; ++part)
+            for (int32_t q = r.q0; q < r.q1; ++q) {
+                seg.push_back(P.mt_seg[q]);
+                seg.back().h_y += part ? (int32_t)low_row : 0;
+            }
+        r.q0 = q0;
+        r.q1 = (int32_t)seg.size();
+        for (int k = 0; k < 2 && r.q0 + k < r.q1; ++k) r.s[k] = seg[r.q0 + k];
+    }
+    P.mt_seg = std::move(seg);
+}
+
 // Extents of every tensor a call reads or writes (see include/plora.h for the layouts).
 struct TensorArgs {
     const void* X = nullptr;
@@ -979,6 +1006,7 @@ struct FwdCall {
     void* saved = nullptr;
     EpiTables ep;              // the projection's epilogue (off for a plain forward)
     HostPlan P;
+    int64_t low_row = 0;       // the first row of H''s low parts (0: none)
     DevPlan D;
     CUtensorMap mZ, mX, mXb, mW, mW128, mPA16, mPA32, mPA64, mPA128, mHk, mHkb, mPBk, mPBk128, mY;
     TcParams q{}, p{};
@@ -1009,7 +1037,7 @@ plora_status fwd_prepare(FwdCall& c, cudaStream_t st, StageCopies& cs) {
               make_map(&c.mPA128, sv + L.o_packA, d_in, (uint64_t)P.n * P.RP, d_in, 64, 128) &&
               make_map(&c.mHk, c.saved, P.RP, P.h_rows, P.RP, 64, kTileM) &&
               make_map(&c.mXb, c.X, d_in, P.T, d_in, 64, kBaseRows) &&
-              make_map(&c.mHkb, c.saved, P.RP, P.h_rows, P.RP, 64, kBaseRows) &&
+              make_map(&c.mHkb, c.saved, P.RP, c.low_row + P.h_rows, P.RP, 64, kBaseRows) &&
               make_packb_map(&c.mPBk, sv + L.o_packB, P.RP, d_out, P.n, kTileN) &&
               make_packb_map(&c.mPBk128, sv + L.o_packB, P.RP, d_out, P.n, kTileM);
     if (!ok) return fail(h, PLORA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
@@ -1020,6 +1048,7 @@ plora_status fwd_prepare(FwdCall& c, cudaStream_t st, StageCopies& cs) {
     q.num_tiles = (int32_t)P.tok.size();
     q.out = c.saved; q.out_ld = P.RP;
     q.out_elems = P.h_rows * P.RP;
+    q.out_low = c.low_row * P.RP;
     q.n_items = (int32_t)P.tok.size();
     // K1 (+K3): Y = X W over all packed tokens; fused, each tile also accumulates H'_j B_j of every
     // adapter j overlapping it, so Y is written once.
@@ -1523,6 +1552,13 @@ plora_status forward_call(plora_ctx* h, const void* X, const void* W, void* Y, i
     c.h = h; c.X = X; c.W = W; c.Y = Y; c.saved = saved;
     c.P = std::move(P);
     c.ep = std::move(ep);
+    if (c.ep.on && relu_low(h, c.ep.act, c.ep.Z != nullptr)) {
+        const size_t bytes = low_bytes_of(h, c.P);
+        if (!in_device_allocation(saved, bytes))
+            return fail(h, PLORA_ERR_INVALID_ARG, "saved is not a device buffer of %zu bytes (plora_epilogue_saved_bytes)", bytes);
+        c.low_row = low_row_of(h, c.P);
+        fold_low_parts(c.P, c.low_row);
+    }
     StageCopies cs{};
     s = fwd_prepare(c, st, cs);
     if (s != PLORA_OK) return s;
@@ -1939,7 +1975,7 @@ plora_status plora_create(plora_handle* out, const plora_config* cfg) {
                     (size_t)round_up(red_max * (int64_t)sizeof(RedEntry), 256) +
                     (size_t)round_up(ops_max * (int64_t)sizeof(SimtOp), 256) +
                     (size_t)round_up((tok_max + 1) * (int64_t)sizeof(MTileRec), 256) +
-                    (size_t)round_up((tok_max + na) * (int64_t)sizeof(LoraSeg), 256) +
+                    (size_t)round_up(2 * (tok_max + na) * (int64_t)sizeof(LoraSeg), 256) +   // (twice: low parts)
                     (size_t)round_up(kDynCounters * (int64_t)sizeof(int32_t), 256) +
                     (size_t)round_up(na * (int64_t)sizeof(void*), 256) * 2 +          // epilogue tables
                     (size_t)round_up(na * (int64_t)sizeof(int32_t), 256) + 1024;
@@ -2072,6 +2108,18 @@ plora_status plora_saved_bytes(plora_handle h, int32_t n, const int64_t* off, co
     HostPlan P;
     build_plan(h, n, off, tab, P);
     *bytes = saved_bytes_of(h, P);
+    return PLORA_OK;
+}
+
+plora_status plora_epilogue_saved_bytes(plora_handle h, int32_t n, const int64_t* off, const plora_adapter* tab,
+                                        const plora_epilogue* ep, size_t* bytes) {
+    const plora_status s = plora_saved_bytes(h, n, off, tab, bytes);
+    if (s != PLORA_OK) return s;
+    if (!ep || ep->activation < PLORA_ACT_NONE || ep->activation > PLORA_ACT_SILU)
+        return fail(h, PLORA_ERR_INVALID_ARG, "no epilogue, or activation out of range");
+    HostPlan P;
+    build_plan(h, n, off, tab, P);
+    if (P.T > 0 && relu_low(h, ep->activation, ep->Z != nullptr)) *bytes = low_bytes_of(h, P);
     return PLORA_OK;
 }
 

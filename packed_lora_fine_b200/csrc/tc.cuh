@@ -132,6 +132,7 @@ struct TcParams {
     int32_t blk_end[kMaxOutBlocks];
     // Extents of what the kernel addresses through plain pointers (checked by the PLORA_DEBUG build).
     int64_t out_elems;      // elements of the output buffer `out`
+    int64_t out_low;        // ShrinkX: from `out` to the low parts of H' (0: none), same rows and pitch
     int64_t part_elems;     // floats of the split partials
     int32_t n_counters;     // ints of the arrival counters
     int32_t n_adapters;     // entries of the adapter table
@@ -310,6 +311,11 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
 __device__ __forceinline__ float2 unpack_bf16x2(uint32_t u) {
     __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162*>(&u);
     return __bfloat1622float2(v);
+}
+// What that rounding left of a and b, rounded in turn (nothing where the rounded value is not finite).
+__device__ __forceinline__ uint32_t pack_bf16x2_low(float a, float b) {
+    const float2 f = unpack_bf16x2(pack_bf16x2(a, b));
+    return pack_bf16x2(fabsf(f.x) <= 3.4e38f ? a - f.x : 0.f, fabsf(f.y) <= 3.4e38f ? b - f.y : 0.f);
 }
 
 // Operand-ring position of one role thread, carried across the work items of a launch.
@@ -774,6 +780,7 @@ __device__ __forceinline__ void epilogue_item(const TcParams& p, const TileInfo&
                                                    (int64_t)(ti.out_row + row + 1) * p.out_ld <= p.out_elems);
         for (int c = 0; c < ti.cols_valid; c += 16) {
             uint4 v0 = make_uint4(0, 0, 0, 0), v1 = make_uint4(0, 0, 0, 0);
+            uint4 w0 = v0, w1 = v0;
             if (c < ti.cols_live) {
                 uint32_t r[16];
                 ptx::tmem_ld16(t_row + c, r);
@@ -788,11 +795,20 @@ __device__ __forceinline__ void epilogue_item(const TcParams& p, const TileInfo&
                     v1.y = pack_bf16x2(s * __uint_as_float(r[10]), s * __uint_as_float(r[11]));
                     v1.z = pack_bf16x2(s * __uint_as_float(r[12]), s * __uint_as_float(r[13]));
                     v1.w = pack_bf16x2(s * __uint_as_float(r[14]), s * __uint_as_float(r[15]));
+                    if (OP == Op::ShrinkX && p.out_low) {
+                        auto low = [&](int k) { return pack_bf16x2_low(s * __uint_as_float(r[k]), s * __uint_as_float(r[k + 1])); };
+                        w0 = make_uint4(low(0), low(2), low(4), low(6));
+                        w1 = make_uint4(low(8), low(10), low(12), low(14));
+                    }
                 }
             }
             if (out_ok) {
                 *reinterpret_cast<uint4*>(out + c) = v0;
                 *reinterpret_cast<uint4*>(out + c + 8) = v1;
+                if (OP == Op::ShrinkX && p.out_low) {
+                    *reinterpret_cast<uint4*>(out + p.out_low + c) = w0;
+                    *reinterpret_cast<uint4*>(out + p.out_low + c + 8) = w1;
+                }
             }
         }
         // The adapter's block has kLoraPad zero rows before and after its (128-rounded) rows, so that
@@ -808,14 +824,17 @@ __device__ __forceinline__ void epilogue_item(const TcParams& p, const TileInfo&
             const bool pads_ok = dcheck(p.err_flag, ad.h_row - kLoraPad >= 0 && p.RP <= p.out_ld &&
                                                         (int64_t)(tail + kLoraPad) * p.out_ld <= p.out_elems);
             for (int pr = row; pr < kLoraPad && pads_ok; pr += kTileM) {
-                if (first) {
-                    uint4* dst = reinterpret_cast<uint4*>(base + (int64_t)(ad.h_row - kLoraPad + pr) * p.out_ld);
-                    for (int c = 0; c < p.RP / 8; ++c) dst[c] = z;
+                for (int part = 0; part < (OP == Op::ShrinkX && p.out_low ? 2 : 1); ++part, base += p.out_low) {
+                    if (first) {
+                        uint4* dst = reinterpret_cast<uint4*>(base + (int64_t)(ad.h_row - kLoraPad + pr) * p.out_ld);
+                        for (int c = 0; c < p.RP / 8; ++c) dst[c] = z;
+                    }
+                    if (last) {
+                        uint4* dst = reinterpret_cast<uint4*>(base + (int64_t)(tail + pr) * p.out_ld);
+                        for (int c = 0; c < p.RP / 8; ++c) dst[c] = z;
+                    }
                 }
-                if (last) {
-                    uint4* dst = reinterpret_cast<uint4*>(base + (int64_t)(tail + pr) * p.out_ld);
-                    for (int c = 0; c < p.RP / 8; ++c) dst[c] = z;
-                }
+                base = static_cast<__nv_bfloat16*>(p.out);
             }
         }
     } else if constexpr (Tr::kExpand) {

@@ -202,6 +202,44 @@ def test_fp32_matches_the_formulas(act):
 
 
 @gpu
+@pytest.mark.parametrize("ranks, counts", [([1], [136]), ([17, 80, 2], [100, 0, 36]), ([3] * 17, [8] * 17)])
+def test_relu_sees_what_a_rounded_h_would_lose(ranks, counts):
+    """relu's derivative jumps with Z's sign, so its training forward takes H' in two bf16 parts.  Here X is the
+    identity, H' = 1.5 A (at most 10 bits), B = 1 and W the negative of H' rounded to 8 bits, so that Z is what that
+    rounding left, without a rounding of its own: it is 0 with H' in one part."""
+    p = Problem("bf16", 136, 264, ranks, counts, bias="none", residual=False, seed=40)
+    p.scales = [1.5] * p.n
+    p.X[:] = torch.eye(136, device="cuda")
+    h = torch.empty(136, device="cuda")
+    for i in range(p.n):
+        p.A[i][1:] = 0
+        p.B[i][:] = 0
+        p.B[i][:, 0] = 1
+        h[int(p.off[i]):int(p.off[i + 1])] = 1.5 * p.A[i][0, int(p.off[i]):int(p.off[i + 1])].float()
+    p.W[:] = -h.bfloat16()
+    left = h - h.bfloat16().float()
+    assert int((left != 0).sum()) > 40
+    eng = p.engine()
+    Y, saved, Z = eng.forward_epilogue(p.X, p.W, p.off, p.scales, p.A, p.B, activation="relu")
+    want = left[:, None].expand(136, 264)
+    assert torch.equal(Z.float(), want) and torch.equal(Y.float(), want.clamp(min=0))
+    dX = eng.backward_epilogue(p.X, p.W, p.dY, p.off, p.scales, p.A, p.B, saved, Z=Z, activation="relu")[0]
+    # the derivative at 0 is 0, and W and the factors cancel in dX: the elementwise bound of the module's docstring
+    dZ = p.dY.double() * (want > 0)
+    for i in range(p.n):
+        t, B, A, W = slice(int(p.off[i]), int(p.off[i + 1])), p.B[i].double(), p.A[i].double(), p.W.double()
+        ref = dZ[t] @ W + 1.5 * (dZ[t] @ B) @ A
+        bound = dZ[t].abs() @ W.abs() + 2 * 1.5 * (dZ[t].abs() @ B.abs()) @ A.abs() + ref.abs()
+        assert inside(dX[t], ref, (U + (264 + 8) * 2.0 ** -24) * bound)
+    # the low parts need room in `saved`, and none without Z
+    tab, ep = eng.table(p.scales, p.A, p.B), pl.make_epilogue("relu", Z=Z.data_ptr())
+    size = lambda e: pl.plora_epilogue_saved_bytes(eng.h, p.n, p.off, tab, e)
+    plain = eng.saved_bytes(p.off, tab)
+    assert size(ep) > plain == size(pl.make_epilogue("relu")) == size(pl.make_epilogue("silu", Z=Z.data_ptr()))
+    eng.close()
+
+
+@gpu
 @pytest.mark.parametrize("act, bias, residual", [("none", "none", True), ("none", "each", False), ("silu", "none", False)])
 def test_each_part_alone(act, bias, residual):
     check(Problem("bf16", 136, 328, [8, 24], [200, 77], bias=bias, residual=residual, seed=5), act)
@@ -591,6 +629,7 @@ def test_refusals_without_a_device():
     lib, out, ep = pl.load(), ctypes.c_size_t(7), pl.make_epilogue("gelu")
     a = ctypes.addressof
     assert lib.plora_epilogue_work_bytes(None, 0, None, a(ep), ctypes.byref(out)) == pl.PLORA_ERR_INVALID_ARG
+    assert lib.plora_epilogue_saved_bytes(None, 0, None, None, a(ep), ctypes.byref(out)) == pl.PLORA_ERR_INVALID_ARG
     assert lib.plora_forward_epilogue(None, None, None, None, 0, None, None, None, a(ep), None) == pl.PLORA_ERR_INVALID_ARG
     assert lib.plora_backward_epilogue(None, None, None, None, None, 0, None, None, None, a(ep), None) == pl.PLORA_ERR_INVALID_ARG
     assert ctypes.sizeof(pl.plora_epilogue) == 48
