@@ -58,7 +58,7 @@ EXPORTED = ("plora_create", "plora_destroy", "plora_saved_bytes", "plora_forward
             "plora_capture_reserve", "plora_capture_release", "plora_partition", "plora_debug_build",
             "plora_layer_create", "plora_layer_destroy", "plora_layer_handle", "plora_layer_saved_bytes",
             "plora_layer_forward", "plora_layer_backward", "plora_layer_check", "plora_layer_last_error",
-            "plora_epilogue_work_bytes", "plora_forward_epilogue", "plora_backward_epilogue",
+            "plora_epilogue_saved_bytes", "plora_epilogue_work_bytes", "plora_forward_epilogue", "plora_backward_epilogue",
             "plora_muon_work_bytes", "plora_muon_step")
 
 
