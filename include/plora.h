@@ -257,7 +257,8 @@ typedef struct {
 PLORA_API plora_status plora_epilogue_work_bytes(plora_handle h, int32_t n_adapters, const int64_t* off,
                                                  const plora_epilogue* ep, size_t* bytes);
 /* Size of `saved` for a forward with this epilogue: plora_saved_bytes(), but more for relu with Z on a bf16 handle,
- * whose forward then takes H' in two bf16 parts (relu's derivative jumps with Z's sign).  Of ep, activation and
+ * whose forward then takes H' in two bf16 parts and computes the Zs next to 0 anew, since relu's derivative jumps with
+ * Z's sign (Y with them, unless there is a residual).  Of ep, activation and
  * whether Z is NULL are read.  The backward reads the first plora_saved_bytes() of it. */
 PLORA_API plora_status plora_epilogue_saved_bytes(plora_handle h, int32_t n_adapters, const int64_t* off,
                                                   const plora_adapter* tab, const plora_epilogue* ep, size_t* bytes);

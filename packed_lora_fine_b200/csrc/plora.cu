@@ -26,6 +26,7 @@
 #include "adamw.cuh"
 #include "epilogue.cuh"
 #include "few.cuh"
+#include "relu.cuh"
 #include "muon.cuh"
 
 using namespace plora;
@@ -227,11 +228,13 @@ __global__ void timeout_probe_kernel(int* err_flag, uint64_t limit_ns) {
 // Kernel kinds for launch accounting / profiling.
 enum Kind { kPack = 0, kBaseFwd, kShrinkX, kExpandY, kBaseDx, kShrinkDy, kExpandDx, kWgradB, kWgradA,
             kSimt, kAdamw, kShrinkDyWgradB, kStage, kBaseDxWgradA, kBaseFwdEp, kFewShrink,
-            kFewBase, kEpilogue, kActGrad, kBiasGrad, kMuonGramK, kMuonNsK, kMuonApplyK, kKinds };
+            kFewBase, kEpilogue, kActGrad, kBiasGrad, kMuonGramK, kMuonNsK, kMuonApplyK,
+            kReluNorms, kReluSigns, kKinds };
 const char* const kKindNames[kKinds] = {"pack_ab", "base_fwd", "shrink_x", "expand_y", "base_dx",
                                         "shrink_dy", "expand_dx", "wgrad_b", "wgrad_a", "simt_gemm", "adamw",
                                         "shrink_dy+wgrad_b", "stage_copy", "base_dx+wgrad_a", "base_fwd_ep",
-                                        "few_shrink", "few_base", "epilogue", "act_grad", "bias_grad", "muon_gram", "muon_ns", "muon_apply"};
+                                        "few_shrink", "few_base", "epilogue", "act_grad", "bias_grad", "muon_gram", "muon_ns", "muon_apply",
+                                        "relu_norms", "relu_signs"};
 static_assert(kKinds <= 32, "plora_ctx::launches and total_ms hold every kind");
 
 cudaEvent_t take_event(plora_ctx* h) {
@@ -425,14 +428,29 @@ SavedLayout saved_layout(const plora_ctx* h, const HostPlan& P) {
 size_t saved_bytes_of(const plora_ctx* h, const HostPlan& P) { return saved_layout(h, P).bytes; }
 
 // relu's derivative jumps where Z changes its sign, so a forward that keeps Z for it takes H' in two bf16 parts,
-// high and low: with H' rounded to bf16 alone, Z is off by 2^-9 of the low-rank part, and as many signs of small
-// Zs with it (10808 -> 544, rank 1 and scale 16: dX 0.0075 off in the 2-norm, 0.002 with both parts).  What is left
-// are the fp32 sums' own errors.  The low parts lie behind the packed
-// factors, in rows of the same pitch: the first of them, and the size of `saved` with them.
+// high and low (with H' rounded to bf16 alone, Z is off by 2^-9 of the low-rank part: 10808 -> 544, rank 1 and scale
+// 16, dX 0.0075 off in the 2-norm, 0.002 with both parts), and computes the Zs anew that the tensor cores' sums leave
+// without a sure sign (relu.cuh).  The low parts lie behind the packed factors, in rows of the same pitch, and
+// the norms that bound Z's errors behind them.
 bool relu_low(const plora_ctx* h, int32_t act, bool keeps_z) { return h->tc && act == PLORA_ACT_RELU && keeps_z; }
 int64_t low_row_of(const plora_ctx* h, const HostPlan& P) { return ceil_div((int64_t)saved_bytes_of(h, P), P.RP * 2); }
+// Where the norms start, each array on 256 bytes (a null base: offsets), and the size of `saved` with them.
+size_t relu_norms(const plora_ctx* h, const HostPlan& P, ReluArgs& a, uint8_t* saved) {
+    size_t at = (size_t)round_up((low_row_of(h, P) + P.h_rows) * P.RP * 2, 256);
+    auto take = [&](float*& p, int64_t count) {
+        p = saved ? reinterpret_cast<float*>(saved + at) : nullptr;
+        at += (size_t)round_up(count * (int64_t)sizeof(float), 256);
+    };
+    take(a.nx, P.T);
+    take(a.nh, P.T);
+    take(a.nw, h->cfg.d_out);
+    take(a.na, (int64_t)P.n * P.RP);
+    take(a.nb, (int64_t)P.n * h->cfg.d_out);
+    return at;
+}
 size_t low_bytes_of(const plora_ctx* h, const HostPlan& P) {
-    return (size_t)(low_row_of(h, P) + P.h_rows) * (size_t)P.RP * 2;
+    ReluArgs a{};
+    return relu_norms(h, P, a, nullptr);
 }
 // Folds each adapter's low parts like another adapter's rows, with the same factor.
 void fold_low_parts(HostPlan& P, int64_t low_row) {
@@ -1073,6 +1091,38 @@ std::vector<int> by_k(const C* calls, int nc, F k_of) {
     return o;
 }
 
+// relu's Zs without a sure sign, computed anew (their bounds' norms first).
+void relu_run(const FwdCall& c, cudaStream_t st) {
+    plora_ctx* h = c.h;
+    ReluArgs a{};
+    a.X = static_cast<const __nv_bfloat16*>(c.X);
+    a.W = static_cast<const __nv_bfloat16*>(c.W);
+    a.H = static_cast<const __nv_bfloat16*>(c.saved);
+    a.low = c.low_row * c.P.RP;
+    a.ad = c.D.ad;
+    a.tok = c.D.tok;
+    a.bias = c.D.bias;
+    a.Y = c.ep.residual ? nullptr : static_cast<__nv_bfloat16*>(c.Y);
+    a.Z = static_cast<__nv_bfloat16*>(c.ep.Z);
+    relu_norms(h, c.P, a, static_cast<uint8_t*>(c.saved));
+    a.d_in = h->cfg.d_in;
+    a.d_out = h->cfg.d_out;
+    a.n = c.P.n;
+    a.RP = c.P.RP;
+    a.tiles = (int32_t)c.P.tok.size();
+    a.blocks.n = h->nblk;
+    for (int b = 0; b < h->nblk; ++b) a.blocks.end[b] = h->blk_end[b];
+    tracked(h, kReluNorms, st, [&] { relu_norms_kernel<<<(unsigned)ceil_div(relu_norm_items(a), 8), 256, 0, st>>>(a); });
+    const int32_t tiles = a.tiles;
+    for (int32_t t0 = 0; t0 < tiles; t0 += 65535) {   // grid.y holds at most 65535 tiles
+        a.tok = c.D.tok + t0;
+        const unsigned ny = (unsigned)std::min(65535, tiles - t0);
+        tracked(h, kReluSigns, st, [&] {
+            relu_signs_kernel<<<dim3((unsigned)ceil_div(a.d_out, kEpiCols), ny), 256, 0, st>>>(a);
+        });
+    }
+}
+
 // The forward of every prepared call: one schedule copy, one pack, one shrink launch, one base-GEMM
 // launch per call (the SM-pair and unfused variants, single calls only, keep their own launches).
 plora_status fwd_launch(FwdCall* calls, int nc, cudaStream_t st, StageCopies& cs) {
@@ -1137,6 +1187,7 @@ plora_status fwd_launch(FwdCall* calls, int nc, cudaStream_t st, StageCopies& cs
                 tracked(h0, kBaseFwdEp, st, [&] {
                     launch_segments<Op::BaseFwd, Op::BaseFwd, true>(S, h0->num_sms, st);
                 });
+                if (c.low_row) relu_run(c, st);
                 continue;
             }
             tracked(h0, kBaseFwd, st, [&] { launch_segments<Op::BaseFwd>(S, h0->num_sms, st); });
