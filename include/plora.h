@@ -367,8 +367,9 @@ PLORA_API plora_status plora_adamw_step(plora_handle h, int32_t n_adapters, cons
  * with k = 1 (PLORA_MUON_SCALE_NONE), sqrt(max(1, rows / cols)) (_ROWS) or 0.2 sqrt(max(rows, cols))
  * (_RMS); then the table's A_i / B_i receive p, rounded to nearest even for bf16.  The usual coefficients
  * are a, b, c = 3.4445, -4.7750, 2.0315 with 5 steps.  X X^T is taken on the short side.  u's
- * two products (its Gram matrix and the final one) take u as the sum of three fp16 numbers, within 2^-27 of
- * its largest element, exactly or in fp32 and joined in fp64 (the first) or fp32; the iteration is in fp64.  A matrix whose u is all zero gets X = 0; one with a
+ * two products (its Gram matrix and the final one) take u as the sum of three fp16 numbers, an integer of its largest
+ * element's leading 8 bits and the next 22 bits of each element, summed in fp32 by order and joined in fp64 (the
+ * first) or fp32; the iteration is in fp64.  A matrix whose u is all zero gets X = 0; one with a
  * NaN or an infinity in u gets X = NaN throughout (other matrices are untouched by it).
  * Adapters are independent, and a matrix's result does not depend on what else is packed with it.
  */

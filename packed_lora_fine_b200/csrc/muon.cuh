@@ -12,13 +12,18 @@
 //
 // Precision.  G squares the condition of u: its small eigenvalues grow by a^2 per step next to a
 // rounding relative to its largest, so a Gram matrix in plain 32-bit sums ends 10 to 100 times further
-// from the formula than iterating on X (simulated over decaying spectra).  G is therefore formed to about
-// 2^-27 and the iteration runs in fp64.  The tensor cores reach that with operands split into three fp16
+// from the formula than iterating on X (simulated over decaying spectra).  G is therefore formed beyond 32 bits
+// and the iteration runs in fp64.  The tensor cores reach that with operands split into three fp16
 // parts, v = x0 + x1 + x2: x0 is v rounded to an integer of at most 8 bits in units of the largest
 // |v| / 256 (or 128), so that the sums of x0 x0 are integers below 2^24 and exact in their fp32
-// accumulator, and x1, x2 are the next 11 bits each.  The seven products of a lower order
-// (x0 x1, x1 x0, x1 x1, x0 x2, x2 x0, x1 x2, x2 x1) share a second accumulator, whose roundings are
-// relative to its own, 2^-8 smaller, sums.
+// accumulator, and x1, x2 are the next 11 bits each, floating: an element far below the largest keeps 22 bits.
+// An accumulator rounds, by up to 2^-23 per step, next to its own sum, so the Gram pass has one for each order of
+// products: x0 x0 | x0 x1, x1 x0 | x1 x1, x0 x2, x2 x0 | x1 x2, x2 x1.  Where a few columns of u dominate (an
+// outlier feature), the rest of u has no x0, its products stand alone in the third, and what the outliers put
+// into the first two is exact; one accumulator for all the lower orders lost the rest in the outliers' roundings (a
+// column 1000 times the others, 128 x 4096: O off by 5e-5, now 1e-6; 32-bit iteration 5e-7).  For the lower parts to
+// keep their bits in fp16 they are scaled by 2^6 and 2^12 there.  Q X_0 takes all products but x2 x2 in two
+// accumulators, x0 x0 and the rest.
 //
 // Tiles.  Both passes work on tiles of 128 rows m x 64 columns l'.  For s > 64 a row is a short-side
 // index c; for s <= 64, J = floor(128 / s) long-side blocks are stacked, m = (j, c), so that a tile holds
@@ -34,6 +39,7 @@
 #include <cuda_fp16.h>
 #include <cuda_bf16.h>
 #include <cstdint>
+#include <type_traits>
 #include "ptx.cuh"
 
 namespace plora {
@@ -95,18 +101,20 @@ __device__ __forceinline__ uint32_t muon_elem_at(int row, int y) {
            (uint32_t)(y & 7) * 2u;
 }
 
-// scale * v = x0 + x1 + x2 (see the top of the file), two values at a time.  |scale v| <= 256, so adding
-// 1.5 2^23 rounds to an integer; scale is a power of two, so the products are exact.
+// scale * v = x0 + x1 / UP + x2 / UP^2 (see the top of the file), two values at a time.  |scale v| <= 256, so adding
+// 1.5 2^23 rounds to an integer; scale and UP are powers of two, so the products are exact.
+template <int UP>
 __device__ __forceinline__ void muon_split2(uint64_t v, uint64_t scale, uint32_t (&h)[3]) {
-    constexpr float kRound = 12582912.f;
+    constexpr float kRound = 12582912.f, kUp = (float)UP;
     const uint64_t round = ptx::f32x2(kRound, kRound), neg = ptx::f32x2(-1.f, -1.f);
     const uint64_t t = ptx::f32x2_fma(v, scale, round);             // x0 + 1.5 2^23
-    const uint64_t n0 = ptx::f32x2_fma(t, neg, round);              // -x0
-    const uint64_t r = ptx::f32x2_fma(v, scale, n0);
+    const uint64_t n0 = ptx::f32x2_fma(t, ptx::f32x2(-kUp, -kUp), ptx::f32x2(kUp * kRound, kUp * kRound));      // -UP x0
+    const uint64_t r = ptx::f32x2_fma(v, UP == 1 ? scale : ptx::f32x2_mul(scale, ptx::f32x2(kUp, kUp)), n0);
     const float2 x0 = ptx::f32x2_get(ptx::f32x2_add(t, ptx::f32x2(-kRound, -kRound))), rr = ptx::f32x2_get(r);
     const __half2 h0 = __floats2half2_rn(x0.x, x0.y), h1 = __floats2half2_rn(rr.x, rr.y);
     const float2 f1 = __half22float2(h1);
-    const float2 x2 = ptx::f32x2_get(ptx::f32x2_fma(ptx::f32x2(f1.x, f1.y), neg, r));
+    const uint64_t left = ptx::f32x2_fma(ptx::f32x2(f1.x, f1.y), neg, r);
+    const float2 x2 = ptx::f32x2_get(UP == 1 ? left : ptx::f32x2_mul(left, ptx::f32x2(kUp, kUp)));
     const __half2 h2 = __floats2half2_rn(x2.x, x2.y);
     h[0] = *reinterpret_cast<const uint32_t*>(&h0);
     h[1] = *reinterpret_cast<const uint32_t*>(&h1);
@@ -318,16 +326,17 @@ struct MuonTile {
             }
         }
     }
-    // The three parts of scale * v into the tile at `base`.  Elements of the tile past the matrix's end are
+    // The three parts of scale * v (scaled by 1, UP and UP^2) into the tile at `base`.  Elements of the tile past the matrix's end are
     // zeros; rows past the matrix's are left alone.
+    template <int UP>
     __device__ __forceinline__ void put(const MuonMat& M, uint32_t base, uint32_t plane, int col0, float scale,
                                         const float (&v)[NQ][4]) const {
         const uint64_t scale2 = ptx::f32x2(scale, scale);
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
             uint32_t a[3], b[3];
-            muon_split2(ptx::f32x2(v[i][0], v[i][1]), scale2, a);
-            muon_split2(ptx::f32x2(v[i][2], v[i][3]), scale2, b);
+            muon_split2<UP>(ptx::f32x2(v[i][0], v[i][1]), scale2, a);
+            muon_split2<UP>(ptx::f32x2(v[i][2], v[i][3]), scale2, b);
             if (mode == kPairs) {
                 if (x < M.J * M.s) {
                     const uint32_t aa = base + muon_elem_at(col0 + row + 2 * i * kPairCols, x);
@@ -354,15 +363,13 @@ struct MuonTile {
     }
 };
 
-// D0 += a0 b0, D1 += the products of a lower order, over one K step; the parts of an operand lie
-// `astep` / `bstep` (in descriptor units of 16 bytes) apart.  FIRST: the products start the accumulators.
-// ALL: x1 x2 and x2 x1 too, 2^-26 of the largest product each: G needs them (its error grows with the iteration),
-// Q X_0 does not.
 struct MuonDesc {
     uint32_t lo, hi;
     __device__ __forceinline__ MuonDesc(uint64_t d) : lo((uint32_t)d), hi((uint32_t)(d >> 32)) {}
 };
-template <bool FIRST, bool ALL>
+// D0 += a0 b0, D1 += the products of a lower order (but a2 b2) over one K step; the parts of an operand lie `astep` / `bstep` (in descriptor units of 16 bytes) apart.  FIRST: the products start
+// the accumulators.
+template <bool FIRST>
 __device__ __forceinline__ void muon_mma(uint32_t d0, uint32_t d1, MuonDesc a, MuonDesc b, uint32_t astep, uint32_t bstep,
                                          uint32_t idesc) {
     ptx::tc_mma_f16_lo<!FIRST>(d0, a.lo, a.hi, b.lo, b.hi, idesc);
@@ -371,10 +378,25 @@ __device__ __forceinline__ void muon_mma(uint32_t d0, uint32_t d1, MuonDesc a, M
     ptx::tc_mma_f16_lo<true>(d1, a.lo + astep, a.hi, b.lo + bstep, b.hi, idesc);
     ptx::tc_mma_f16_lo<true>(d1, a.lo, a.hi, b.lo + 2 * bstep, b.hi, idesc);
     ptx::tc_mma_f16_lo<true>(d1, a.lo + 2 * astep, a.hi, b.lo, b.hi, idesc);
-    if constexpr (ALL) {
-        ptx::tc_mma_f16_lo<true>(d1, a.lo + astep, a.hi, b.lo + 2 * bstep, b.hi, idesc);
-        ptx::tc_mma_f16_lo<true>(d1, a.lo + 2 * astep, a.hi, b.lo + bstep, b.hi, idesc);
-    }
+    ptx::tc_mma_f16_lo<true>(d1, a.lo + astep, a.hi, b.lo + 2 * bstep, b.hi, idesc);
+    ptx::tc_mma_f16_lo<true>(d1, a.lo + 2 * astep, a.hi, b.lo + bstep, b.hi, idesc);
+}
+// The Gram pass's, a tile with itself: four accumulators of 128 columns (see the top of the file).
+template <bool FIRST>
+__device__ __forceinline__ void muon_gram_mma(uint32_t d, MuonDesc a, uint32_t step, uint32_t idesc) {
+    auto mma = [&](auto first, int acc, uint32_t i, uint32_t j) {
+        ptx::tc_mma_f16_lo<!decltype(first)::value>(d + acc * 128, a.lo + i * step, a.hi, a.lo + j * step, a.hi, idesc);
+    };
+    constexpr std::integral_constant<bool, FIRST> first{};
+    constexpr std::false_type more{};
+    mma(first, 0, 0, 0);
+    mma(first, 1, 0, 1);
+    mma(more, 1, 1, 0);
+    mma(first, 2, 1, 1);
+    mma(more, 2, 0, 2);
+    mma(more, 2, 2, 0);
+    mma(first, 3, 1, 2);
+    mma(more, 3, 2, 1);
 }
 
 // ---------------------------------------------------------------------------------------------- Gram
@@ -392,6 +414,7 @@ constexpr int kGramStage = 3 * kMuonPlane;
 constexpr int kGramRaw = 128 * kMuonTileL * 8; // a tile's g and m
 constexpr int kGramSmem = 2 * kGramStage + 2 * kGramRaw + 1024;
 static_assert(kGramSmem + 1024 <= 232448, "shared memory per CTA");
+constexpr int kGramUp = 64;             // the lower parts' factor: the accumulators are in units of 1, 2^-6, 2^-12 and 2^-18
 constexpr int kGramExactTiles = 16;     // tiles whose x0 x0 sums stay below 2^24 (|x0| <= 128, 64 columns each)
 
 // One item: the partial Gram matrix (of its two equal halves the elements [c][r], c <= r) of a run of tiles
@@ -399,7 +422,7 @@ constexpr int kGramExactTiles = 16;     // tiles whose x0 x0 sums stay below 2^2
 // (two tiles ahead, every thread its own elements) and split u into one of two places; a further warp issues a place's products.
 // The scale of the split is a power of two, 1.5 to 3 times the first tile's largest |u|.  A tile that exceeds it
 // takes the sums out of the accumulators and starts them anew at its own scale, and so does every 16th tile.
-// 8 bytes per element: 32 adapters of rank 8 to 128 at 4096 -> 14336 (40 M elements) take 176 us for the bytes' 49, 3.5
+// 8 bytes per element: 32 adapters of rank 8 to 128 at 4096 -> 14336 (40 M elements) take 191 us for the bytes' 49, 3.5
 // us per tile (1.1 of them the products') and 7 per item to begin and to take the sums out; what bounds a tile is the
 // chain from its copies through the split and the proxy fence to its products, one tile at a time over the block.
 __global__ void __launch_bounds__(kGramThreads, 1)
@@ -427,7 +450,7 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
         ptx::fence_barrier_init();
     }
     if (warp == kGramLoad / 32) {
-        ptx::tmem_alloc<256>(&tmem_slot);
+        ptx::tmem_alloc<512>(&tmem_slot);
         ptx::tmem_relinquish();
     }
     // rows past the matrix's stay zero (their products reach no output, but must not be NaN)
@@ -486,25 +509,30 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
             for (int c0 = part * 16; c0 < 128; c0 += 64) {     // the four warps of these rows take turns
                 // only columns up to the warp's last row are needed
                 if (c0 > (warp & 3) * 32 + 31) break;
-                uint32_t hi[16], lo[16];
-                ptx::tmem_ld16(t_row + c0, hi);
-                ptx::tmem_ld16(t_row + 128 + c0, lo);
-                ptx::tmem_ld_wait();
                 // a diagonal block is in several pairs: the pair with the next group writes it (the last group's, the
                 // pair with the one before)
                 const int gr = r < 64 ? ga : gb, gc = c0 < 64 ? ga : gb, rr = gr * 64 + (r & 63);
                 const bool own = (gr != gc || (gr == ga ? gb == ga + 1 : ga == ng - 2)) && rr < M.s;
                 double* const o = out + (gc * 64 + (c0 & 63)) * M.s + rr;      // lanes on consecutive addresses
                 const int cols = min(16, M.s - (gc * 64 + (c0 & 63)));
+#pragma unroll 1
+                for (int k0 = 0; k0 < 16; k0 += 8) {
+                    uint32_t d[4][8];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const int c = c0 + k;
-                    if (c > r) continue;
-                    const double v = muon_to_double(__uint_as_float(hi[k]), k2) + muon_to_double(__uint_as_float(lo[k]), k2);
-                    if (M.J > 1) {
-                        if (j < M.J && c >= j * M.s) stack[(c - j * M.s) * 128 + r] = v;
-                    } else if (own && k < cols) {
-                        o[k * M.s] = stored ? o[k * M.s] + v : v;
+                    for (int q = 0; q < 4; ++q) ptx::tmem_ld8(t_row + q * 128 + c0 + k0, d[q]);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int c = c0 + k0 + k;
+                        if (c > r) continue;
+                        const float low = fmaf(__uint_as_float(d[3][k]), 1.f / kGramUp, __uint_as_float(d[2][k]));
+                        const double v = muon_to_double(__uint_as_float(d[0][k]), k2) + (muon_to_double(__uint_as_float(d[1][k]), k2 - 6) +
+                                                                                        muon_to_double(low, k2 - 12));
+                        if (M.J > 1) {
+                            if (j < M.J && c >= j * M.s) stack[(c - j * M.s) * 128 + r] = v;
+                        } else if (own && k0 + k < cols) {
+                            o[(k0 + k) * M.s] = stored ? o[(k0 + k) * M.s] + v : v;
+                        }
                     }
                 }
             }
@@ -599,7 +627,7 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
             if (bad) break;                     // a NaN or an infinity: the whole matrix becomes NaN
             if (scale == 0.f) continue;         // nothing but zeros so far
             if (count >= 2) wait_step(count - 2);              // the products that last read this place
-            T.put(M, s0 + (count & 1) * kGramStage, kMuonPlane, 0, scale, u);
+            T.put<kGramUp>(M, s0 + (count & 1) * kGramStage, kMuonPlane, 0, scale, u);
             hand_over(since == 0 ? kStart : kAdd);
             ++since;
         }
@@ -642,12 +670,12 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
             const MuonDesc d0 = tall ? ptx::smem_desc_sw128(base, 8192, 1024) : ptx::smem_desc_sw128(base, 16, 1024);
             if (one) {
                 MuonDesc d = d0;
-                if (todo == kStart) muon_mma<true, true>(tmem, tmem + 128, d, d, kMuonPlane / 16, kMuonPlane / 16, idesc);
-                else muon_mma<false, true>(tmem, tmem + 128, d, d, kMuonPlane / 16, kMuonPlane / 16, idesc);
+                if (todo == kStart) muon_gram_mma<true>(tmem, d, kMuonPlane / 16, idesc);
+                else muon_gram_mma<false>(tmem, d, kMuonPlane / 16, idesc);
 #pragma unroll
                 for (int q = 1; q < kMuonTileL / 16; ++q) {
                     d.lo += kstep;
-                    muon_mma<false, true>(tmem, tmem + 128, d, d, kMuonPlane / 16, kMuonPlane / 16, idesc);
+                    muon_gram_mma<false>(tmem, d, kMuonPlane / 16, idesc);
                 }
                 ptx::tc_commit(&done[place]);
             }
@@ -658,7 +686,7 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (warp == kGramLoad / 32) ptx::tmem_dealloc<256>(tmem);
+    if (warp == kGramLoad / 32) ptx::tmem_dealloc<512>(tmem);
 }
 
 // ----------------------------------------------------------------------------------------- iteration
@@ -1191,8 +1219,8 @@ static_assert(kApplySmem + 1024 <= 232448, "shared memory per CTA");
 //            accumulators, of two such sets in turn
 //   finish   p to shared memory (two blocks ahead), O out of the accumulators onto it, the new p and its copy
 // BIG (s > 128): tiles of 256 rows in one place, Q's (row half, column block) pieces streamed from L2.
-// 22 bytes per element: 32 adapters of rank 8 to 128 at 4096 -> 14336 (40 M elements) take 268 us for the bytes' 134,
-// 65536 x 128 matrices alone (67 M) 336 for 225; odd short sides cost most (their rows start off 16 bytes).  BIG: 146
+// 22 bytes per element: 32 adapters of rank 8 to 128 at 4096 -> 14336 (40 M elements) take 279 us for the bytes' 134,
+// 65536 x 128 matrices alone (67 M, six products) 336 for 225; odd short sides cost most (their rows start off 16 bytes).  BIG: 160
 // for 56.  Bound by the roles sharing an SM: of the 336, 209 are left without p's traffic, 182 without the stores of m
 // and the split as well, 157 without the products, and 181 with everything but the traffic.  Loads of a step ahead in
 // registers did not help (342).
@@ -1314,7 +1342,7 @@ muon_apply_kernel(const MuonMat* __restrict__ mats, int first, int last, int til
                         --unclean;
                     }
                 }
-                T.put(C, base, PLANE, st * STEP, xs, g);
+                T.template put<1>(C, base, PLANE, st * STEP, xs, g);
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
@@ -1588,13 +1616,13 @@ muon_apply_kernel(const MuonMat* __restrict__ mats, int first, int last, int til
             if constexpr (!BIG) {
                 const MuonDesc q0 = ptx::smem_desc_sw128(sq0, 16, 1024);
                 if (one) {
-                muon_mma<true, false>(d0, d0 + 64, q0, v0, kMuonPlane / 16, PLANE / 16, idesc);
+                muon_mma<true>(d0, d0 + 64, q0, v0, kMuonPlane / 16, PLANE / 16, idesc);
 #pragma unroll
                 for (int ks = 1; ks < 8; ++ks) {
                     if (ks >= ksteps) break;
                     MuonDesc d = q0;
                     d.lo += (uint32_t)((ks >> 2) * 3 * kMuonPlane + (ks & 3) * 32) / 16;
-                    muon_mma<false, false>(d0, d0 + 64, d, v_at(ks), kMuonPlane / 16, PLANE / 16, idesc);
+                    muon_mma<false>(d0, d0 + 64, d, v_at(ks), kMuonPlane / 16, PLANE / 16, idesc);
                 }
                 }
             } else {
@@ -1621,8 +1649,8 @@ muon_apply_kernel(const MuonMat* __restrict__ mats, int first, int last, int til
                         if (b * 4 + ks >= ksteps) break;
                         MuonDesc d = q0;
                         d.lo += ks * 2;
-                        if (ks == 0 && b == 0) muon_mma<true, false>(dh, dh + 64, d, v_at(0), kMuonPlane / 16, PLANE / 16, idesc);
-                        else muon_mma<false, false>(dh, dh + 64, d, v_at(b * 4 + ks), kMuonPlane / 16, PLANE / 16, idesc);
+                        if (ks == 0 && b == 0) muon_mma<true>(dh, dh + 64, d, v_at(0), kMuonPlane / 16, PLANE / 16, idesc);
+                        else muon_mma<false>(dh, dh + 64, d, v_at(b * 4 + ks), kMuonPlane / 16, PLANE / 16, idesc);
                     }
                     ptx::tc_commit(&qfree[n & 1]);
                     }
