@@ -618,7 +618,8 @@ muon_gram_kernel(const MuonMat* __restrict__ mats, int n, int* err_flag, uint64_
                     for (int k = 0; k < kGramLoad / 32; ++k) w = fmaxf(w, red[k]);
                     if (!bad && w > 0.f) {
                         // a power of two at least 1.5 times the largest, so that the next steps' seldom exceed it
-                        unit = max(ilogbf(1.5f * w) + 1, -100) - 7;
+                        // (1.5 w itself may be past the largest float)
+                        unit = max(ilogbf(0.75f * w) + 2, -100) - 7;
                         scale = scalbnf(1.f, -unit);
                     }
                     sync();

@@ -57,3 +57,19 @@ def test_outliers(kind, factor, d_in):
         err = float((got.double() - o).norm()) / float(o.norm())
         assert err <= (128 + min(u.shape) / 2) * 2.0 ** -24, (tuple(u.shape), err)
     eng.close()
+
+
+@gpu
+@pytest.mark.parametrize("largest", [1.7e38, 2.3e38, 3.4e38, 1e-20])
+def test_the_largest_floats(largest):
+    """u up to the end of fp32 (eps is nothing next to it, or, at 1e-20, everything): no scale overflows."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    ranks = [5, 100, 200]
+    gA = [torch.randn(r, 1000, generator=g, device="cuda").clamp(-4, 4) * (largest / 4) for r in ranks]
+    gB = [torch.randn(264, r, generator=g, device="cuda").clamp(-4, 4) * (largest / 4) for r in ranks]
+    gA[0][1, 3] = gB[1][263, 99] = largest
+    eng = pl.PackedLoRA(1000, 264, "fp32", max_adapters=len(ranks), max_rank=256, max_tokens=16)
+    for got, u in zip(orthogonalised(eng, ranks, gA, gB), gA + gB):
+        o = orth64(u)
+        assert float((got.double() - o).norm()) <= (128 + min(u.shape) / 2) * 2.0 ** -24 * float(o.norm()), tuple(u.shape)
+    eng.close()
