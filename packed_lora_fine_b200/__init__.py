@@ -574,6 +574,14 @@ class PackedLoRA:
                 raise ValueError(f"{name}: a contiguous {dt} tensor of shape {want} is needed, got {t.dtype} "
                                  f"{tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous'}")
 
+    @staticmethod
+    def _tokens(X, off) -> int:
+        """off[-1], the rows of X that belong to an adapter; ValueError where X has fewer."""
+        T = int(off[-1])
+        if T > X.shape[0]:
+            raise ValueError(f"off: the last adapter ends at row {T}, X has {X.shape[0]}")
+        return T
+
     def _check_factors(self, A, B, n):
         import torch
         dt = torch.bfloat16 if self.dtype == "bf16" else torch.float32
@@ -606,15 +614,18 @@ class PackedLoRA:
         activation: a name in ``ACTIVATIONS``; residual: ``[T][d_out]`` (with a bf16 engine it may be the tensor
         given as Y).
         Z is the pre-activation that ``backward_epilogue`` needs with an activation (None without one).
+        X may have rows behind off[-1]: a Y that is given keeps what it has there, a new one (and Z) is zero there.
         want_Z false: an inference call, which keeps nothing for a backward.  saved and Z are then None, and up to 32
         tokens of a bf16 engine go through kernels for few tokens (sums in another order than a training call's)."""
         import torch
         n = len(off) - 1
+        T = self._tokens(X, off)
         self._check_tensors(X.shape[0], X=X, W=W, residual=residual, Y=Y)
         bias = self._bias_list(bias, n)
         self._check_factors(A, B, n)
         tab = self.table(scales, A, B)
-        if Y is None:
+        new = Y is None
+        if new:
             Y = torch.empty((X.shape[0], self.d_out), dtype=X.dtype, device=X.device)
         Z = torch.empty_like(Y) if want_Z and activation != "none" else None
         ep = make_epilogue(activation, None if bias is None else [b.data_ptr() if b is not None else None for b in bias],
@@ -622,6 +633,11 @@ class PackedLoRA:
                            Z=Z.data_ptr() if Z is not None else None, inference=not want_Z)
         if saved is None:
             saved = torch.empty(max(plora_epilogue_saved_bytes(self.h, n, off, tab, ep), 256), dtype=torch.uint8, device=X.device)
+        if T < X.shape[0]:
+            with torch.cuda.stream(stream):
+                for t in (Y if new else None, Z):
+                    if t is not None:
+                        t[T:].zero_()
         st = (stream or torch.cuda.current_stream(X.device)).cuda_stream
         plora_forward_epilogue(self.h, X.data_ptr(), W.data_ptr(), Y.data_ptr(), n, off, tab, saved.data_ptr(), ep, st)
         if not want_Z and stream is not None:     # scratch that goes back to the allocator while the stream may use it
@@ -633,9 +649,10 @@ class PackedLoRA:
         """The backward of ``forward_epilogue``: returns (dX, dA, dB, dbias).  dX is None without want_dX;
         dbias is a list of fp32 ``[d_out]`` tensors, one per adapter, or None; want_dbias may be a list of
         truth values, one per adapter (dbias[i] is then None where it is false).  The residual's gradient
-        is dY."""
+        is dY (in the rows of an adapter; dX is zero behind off[-1])."""
         import torch
         n = len(off) - 1
+        self._tokens(X, off)
         self._check_tensors(X.shape[0], X=X, W=W, dY=dY, Z=Z)
         self._check_factors(A, B, n)
         f32 = dict(dtype=torch.float32, device=X.device)
@@ -652,6 +669,9 @@ class PackedLoRA:
         import torch
         n = len(off) - 1
         dX = torch.empty_like(X) if want_dX else None
+        if want_dX and self._tokens(X, off) < X.shape[0]:
+            with torch.cuda.stream(stream):
+                dX[int(off[-1]):].zero_()
         tab = make_table([b.shape[1] for b in B], scales, [a.data_ptr() for a in A], [b.data_ptr() for b in B], pA, pB)
         ep = make_epilogue(activation, dbias=pb, Z=Z.data_ptr() if Z is not None else None)
         nbytes = plora_epilogue_work_bytes(self.h, n, off, ep)
@@ -803,6 +823,8 @@ def _packed_lora_fn():
             X_, W_, Z = X_.contiguous(), W_.contiguous(), None
             if call.plain:
                 Y, saved = call.engine.forward(X_, W_, call.off, call.scales, A_, B_)
+                if int(call.off[-1]) < Y.shape[0]:
+                    Y[int(call.off[-1]):].zero_()
             else:
                 Y, saved, Z = call.engine.forward_epilogue(X_, W_, call.off, call.scales, A_, B_,
                                                            bias=[None if k is None else b_[k] for k in call.where],
@@ -826,8 +848,11 @@ def _packed_lora_fn():
             counts = [t.numel() for t in AB] + [dY.shape[1]] * len(owners)
             flat = torch.empty(sum(counts), dtype=torch.float32, device=dY.device)
             ptrs = list(itertools.accumulate(counts, lambda at, c: at + 4 * c, initial=flat.data_ptr()))
+            T = int(call.off[-1])
             if call.plain:
                 dX = torch.empty_like(X_) if want_dX else None
+                if want_dX and T < dX.shape[0]:
+                    dX[T:].zero_()
                 tab = make_table([b.shape[1] for b in B_], call.scales, [a.data_ptr() for a in A_], [b.data_ptr() for b in B_],
                                  ptrs[:n], ptrs[n:2 * n])
                 plora_backward(call.engine.h, X_.data_ptr(), W_.data_ptr(), dY.contiguous().data_ptr(),
@@ -845,7 +870,10 @@ def _packed_lora_fn():
                     own = [2 * n + j for j, i in enumerate(owners) if call.where[i] == k]
                     gb[k] = g[own[0]] if len(own) == 1 else torch.stack([flat.split(counts)[j] for j in own]).sum(0).to(dY.dtype)
             g = [x.view(t.shape) for x, t in zip(g, AB)]
-            return (None, dX, None, dY if ctx.needs_input_grad[3] else None, *g, *gb)
+            dR = dY if ctx.needs_input_grad[3] else None
+            if dR is not None and T < dR.shape[0]:
+                dR = torch.cat([dR[:T], torch.zeros_like(dR[T:])])
+            return (None, dX, None, dR, *g, *gb)
 
     return PackedLoRAFn
 
@@ -856,9 +884,11 @@ def packed_lora(engine: "PackedLoRA", X, W, off, scales, A, B, bias=None, activa
     ([r_i][d_in]), B[i] is lora_B.weight ([d_out][r_i]), W is nn.Linear.weight ([d_out][d_in]); `off` holds
     the host segment offsets of the packed rows of X.  bias: None, one [d_out] tensor that every adapter
     shares (its gradient sums over the adapters) or a list with one (or None) per adapter; activation: a
-    name in ACTIVATIONS; residual: [T][d_out].  Without these three the backward runs plora_backward, else
+    name in ACTIVATIONS; residual: [T][d_out].  Rows of X behind off[-1] belong to no adapter: Y is zero there, and so are
+    the gradients of X and residual.  Without these three the backward runs plora_backward, else
     plora_backward_epilogue; the fp32 weight gradients are returned in each parameter's dtype."""
     n = len(off) - 1
+    engine._tokens(X, off)
     plain = bias is None and activation == "none" and residual is None
     per_adapter = [None] * n if bias is None else engine._bias_list(bias, n)
     uniq = list({id(b): b for b in per_adapter if b is not None}.values())   # a shared bias is one input
