@@ -849,20 +849,21 @@ def _packed_lora_fn():
             flat = torch.empty(sum(counts), dtype=torch.float32, device=dY.device)
             ptrs = list(itertools.accumulate(counts, lambda at, c: at + 4 * c, initial=flat.data_ptr()))
             T = int(call.off[-1])
+            dY = dY.contiguous()        # (kept until the launches are behind it: their arguments are pointers)
             if call.plain:
                 dX = torch.empty_like(X_) if want_dX else None
                 if want_dX and T < dX.shape[0]:
                     dX[T:].zero_()
                 tab = make_table([b.shape[1] for b in B_], call.scales, [a.data_ptr() for a in A_], [b.data_ptr() for b in B_],
                                  ptrs[:n], ptrs[n:2 * n])
-                plora_backward(call.engine.h, X_.data_ptr(), W_.data_ptr(), dY.contiguous().data_ptr(),
+                plora_backward(call.engine.h, X_.data_ptr(), W_.data_ptr(), dY.data_ptr(),
                                dX.data_ptr() if want_dX else None, n, call.off, tab, saved.data_ptr(),
                                torch.cuda.current_stream().cuda_stream)
             else:
                 pb = [None] * n
                 for i, at in zip(owners, ptrs[2 * n:]):
                     pb[i] = at
-                dX = call.engine._gradients(X_, W_, dY.contiguous(), call.off, call.scales, A_, B_, saved, Z, call.activation,
+                dX = call.engine._gradients(X_, W_, dY, call.off, call.scales, A_, B_, saved, Z, call.activation,
                                             want_dX, ptrs[:n], ptrs[n:2 * n], pb if owners else None)
             g = list((flat if flat.dtype == dY.dtype else flat.to(dY.dtype)).split(counts)) if counts else []
             for k, need in enumerate(need_b):       # a shared bias sums its adapters' fp32 gradients
