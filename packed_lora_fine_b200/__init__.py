@@ -887,7 +887,9 @@ def packed_lora(engine: "PackedLoRA", X, W, off, scales, A, B, bias=None, activa
     shares (its gradient sums over the adapters) or a list with one (or None) per adapter; activation: a
     name in ACTIVATIONS; residual: [T][d_out].  Rows of X behind off[-1] belong to no adapter: Y is zero there, and so are
     the gradients of X and residual.  Without these three the backward runs plora_backward, else
-    plora_backward_epilogue; the fp32 weight gradients are returned in each parameter's dtype."""
+    plora_backward_epilogue; the fp32 weight gradients are returned in each parameter's dtype.  The gradients of A, B and
+    bias of one call are views of one buffer (one launch casts them all): each starts on 16 bytes, and one that is kept
+    or saved keeps the buffer; clone it to have it alone."""
     n = len(off) - 1
     engine._tokens(X, off)
     plain = bias is None and activation == "none" and residual is None
