@@ -81,12 +81,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
-// The same for waits of whole blocks: the timer, a slow read, is only started after many tries.
+// The same for waits of whole warps: the timer, a slow read, is only started after many tries.  Every lane polls, so
+// the warp comes together again before it goes on to instructions that need all of it (tcgen05.ld, mma.sync, an
+// aligned barrier), with one answer: a wait that ran out for one lane ran out for the warp.
 __device__ __forceinline__ bool mbar_wait_many(uint64_t* bar, uint32_t parity, volatile int* abort,
                                                uint64_t limit_ns, int* err_flag) {
-    for (int it = 0; it < 1024; ++it)
-        if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait(bar, parity, abort, limit_ns, err_flag);
+    bool ok = false;
+    for (int it = 0; it < 1024 && !ok; ++it) ok = mbar_try_wait(bar, parity);
+    if (!ok) ok = mbar_wait(bar, parity, abort, limit_ns, err_flag);
+    return __all_sync(0xffffffffu, ok);
 }
 
 // -------------------------------------------------------------------- TMA
