@@ -241,7 +241,9 @@ typedef enum {
  * inference 1: a forward without a backward.  Z is NULL, and `saved`, of plora_saved_bytes(), is scratch
  * that holds nothing afterwards.  With a bf16 handle and at most 32 tokens such a call reads W once in kernels for
  * few tokens, takes no schedule slot (a capture needs none reserved for it) and sums in another order than a
- * training call; a token's result does not depend on the call's other tokens within 32, or above.
+ * training call; a token's result does not depend on the call's other tokens within 32, or above.  Above 32 tokens Y is
+ * a training call's to the bit but for relu, whose training call takes H' in two bf16 parts where this one rounds
+ * it: Y differs by up to 2^-8 of |H'||B| then, as any other activation's does from the formula.
  */
 typedef struct {
     int32_t activation;

@@ -616,7 +616,8 @@ class PackedLoRA:
         Z is the pre-activation that ``backward_epilogue`` needs with an activation (None without one).
         X may have rows behind off[-1]: a Y that is given keeps what it has there, a new one (and Z) is zero there.
         want_Z false: an inference call, which keeps nothing for a backward.  saved and Z are then None, and up to 32
-        tokens of a bf16 engine go through kernels for few tokens (sums in another order than a training call's)."""
+        tokens of a bf16 engine go through kernels for few tokens (sums in another order than a training call's); above,
+        Y is a training call's, but for relu on a bf16 engine, whose training call does not round X A to bf16."""
         import torch
         n = len(off) - 1
         T = self._tokens(X, off)
