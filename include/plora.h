@@ -236,8 +236,8 @@ typedef enum {
  * written by the forward (NULL: not kept), read by the backward of an activation.  work: the backward's
  * scratch, plora_epilogue_work_bytes() bytes, 256-byte aligned (may be NULL if that is 0).  The forward
  * ignores dbias and work, the backward bias and residual (dR is dY).  Every other pointer is 16-byte
- * aligned.  A buffer that a call writes must not overlap another of these buffers, Y, dY or dX
- * (PLORA_ERR_INVALID_ARG), except residual = Y.
+ * aligned.  A buffer that a call writes must not overlap another of its buffers, X, W, saved, the factors and their
+ * gradients among them (PLORA_ERR_INVALID_ARG), except residual = Y.
  * inference 1: a forward without a backward.  Z is NULL, and `saved`, of plora_saved_bytes(), is scratch
  * that holds nothing afterwards.  With a bf16 handle and at most 32 tokens such a call reads W once in kernels for
  * few tokens, takes no schedule slot (a capture needs none reserved for it) and sums in another order than a

@@ -1411,8 +1411,8 @@ plora_status bwd_launch(BwdCall* calls, int nc, cudaStream_t st, StageCopies& cs
 }
 
 // The checks of a forward's (dY: the call's Y) or a backward's epilogue; fills the tables its kernels read.
-plora_status epilogue_args(plora_ctx* h, const HostPlan& P, const plora_epilogue& e, bool backward, const void* Y,
-                           const void* dX, EpiTables& ep) {
+plora_status epilogue_args(plora_ctx* h, const HostPlan& P, const plora_epilogue& e, bool backward, const plora_adapter* tab,
+                           const void* X, const void* W, const void* Y, const void* dX, const void* saved, EpiTables& ep) {
     if (!h->tc && h->cfg.dtype != PLORA_FP32)
         return fail(h, PLORA_ERR_UNSUPPORTED, "an epilogue needs an fp32 handle or the tensor-core path");
     if (h->cfg.flags & (PLORA_FLAG_UNFUSED | PLORA_FLAG_BASE_PAIR))
@@ -1452,8 +1452,27 @@ plora_status epilogue_args(plora_ctx* h, const HostPlan& P, const plora_epilogue
         }
     }
     if (s != PLORA_OK) return s;
+    // the call's other buffers (their extents have been checked)
+    auto span = [&](const void* p, size_t bytes, bool write) {
+        spans.push_back(Span{reinterpret_cast<uintptr_t>(p), bytes, write});
+    };
+    const size_t xbytes = (size_t)P.T * (size_t)h->cfg.d_in * es;
+    for (int32_t i = 0; i < P.n; ++i) {
+        const size_t ra = (size_t)tab[i].rank * (size_t)h->nblk * (size_t)h->cfg.d_in, rb = (size_t)tab[i].rank * d_out;
+        if (backward) {
+            span(tab[i].dA, ra * sizeof(float), true);
+            span(tab[i].dB, rb * sizeof(float), true);
+        }
+        if (P.T > 0) {
+            span(tab[i].A, ra * es, false);
+            span(tab[i].B, rb * es, false);
+        }
+    }
     if (P.T > 0) {
-        spans.push_back(Span{reinterpret_cast<uintptr_t>(Y), ybytes, !backward});
+        span(X, xbytes, false);
+        span(W, (size_t)h->cfg.d_in * d_out * es, false);
+        span(saved, relu_low(h, e.activation, !backward && e.Z) ? low_bytes_of(h, P) : saved_bytes_of(h, P), !backward);
+        span(Y, ybytes, !backward);
         if (!backward) {
             ep.residual = e.residual;
             ep.Z = e.Z;
@@ -1475,13 +1494,12 @@ plora_status epilogue_args(plora_ctx* h, const HostPlan& P, const plora_epilogue
                 s = buffer(e.work, wb, 256, true, "work");
                 ep.work = e.work;
             }
-            if (s == PLORA_OK && dX)
-                spans.push_back(Span{reinterpret_cast<uintptr_t>(dX), (size_t)P.T * (size_t)h->cfg.d_in * es, true});
+            if (s == PLORA_OK && dX) span(dX, xbytes, true);
         }
         if (s != PLORA_OK) return s;
     }
     if (spans_clash(spans))
-        return fail(h, PLORA_ERR_INVALID_ARG, "a buffer that the call writes overlaps another of its epilogue's buffers");
+        return fail(h, PLORA_ERR_INVALID_ARG, "a buffer that the call writes overlaps another of its buffers");
     int32_t t0 = 0;
     ep.tile0.resize(P.n);
     for (int32_t i = 0; i < P.n; ++i) {
@@ -1556,7 +1574,7 @@ plora_status forward_call(plora_ctx* h, const void* X, const void* W, void* Y, i
     if (s != PLORA_OK) return s;
     EpiTables ep;
     if (epi) {
-        s = epilogue_args(h, P, *epi, false, Y, nullptr, ep);
+        s = epilogue_args(h, P, *epi, false, tab, X, W, Y, nullptr, saved, ep);
         if (s != PLORA_OK) return s;
     }
     if (P.T == 0) return PLORA_OK;
@@ -1627,7 +1645,7 @@ plora_status backward_call(plora_ctx* h, const void* X, const void* W, const voi
     if (s != PLORA_OK) return s;
     EpiTables ep;
     if (epi) {
-        s = epilogue_args(h, P, *epi, true, dY, dX, ep);
+        s = epilogue_args(h, P, *epi, true, tab, X, W, dY, dX, saved, ep);
         if (s != PLORA_OK) return s;
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
