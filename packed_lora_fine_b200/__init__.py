@@ -582,6 +582,21 @@ class PackedLoRA:
             raise ValueError(f"off: the last adapter ends at row {T}, X has {X.shape[0]}")
         return T
 
+    @staticmethod
+    def _launch_stream(stream, device):
+        """The stream of a call, and the same if it is not the current one, else None.  A call's new tensors come from the
+        current stream's memory, where work on what was there before may not have ended: another stream waits for it
+        (one that is being captured cannot: its capture holds what it needs)."""
+        import torch
+        current = torch.cuda.current_stream(device)
+        if stream is None or stream == current:
+            return current, None
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return stream, None
+        stream.wait_stream(current)
+        return stream, stream
+
     def _check_factors(self, A, B, n):
         import torch
         dt = torch.bfloat16 if self.dtype == "bf16" else torch.float32
@@ -615,6 +630,7 @@ class PackedLoRA:
         given as Y).
         Z is the pre-activation that ``backward_epilogue`` needs with an activation (None without one).
         X may have rows behind off[-1]: a Y that is given keeps what it has there, a new one (and Z) is zero there.
+        stream: a torch stream to launch on, behind the current one's work so far (None: the current one).
         want_Z false: an inference call, which keeps nothing for a backward.  saved and Z are then None, and up to 32
         tokens of a bf16 engine go through kernels for few tokens (sums in another order than a training call's); above,
         Y is a training call's, but for relu on a bf16 engine, whose training call does not round X A to bf16."""
@@ -632,17 +648,20 @@ class PackedLoRA:
         ep = make_epilogue(activation, None if bias is None else [b.data_ptr() if b is not None else None for b in bias],
                            residual=residual.data_ptr() if residual is not None else None,
                            Z=Z.data_ptr() if Z is not None else None, inference=not want_Z)
-        if saved is None:
+        own = saved is None
+        if own:
             saved = torch.empty(max(plora_epilogue_saved_bytes(self.h, n, off, tab, ep), 256), dtype=torch.uint8, device=X.device)
+        st, other = self._launch_stream(stream, X.device)
         if T < X.shape[0]:
-            with torch.cuda.stream(stream):
+            with torch.cuda.stream(st):
                 for t in (Y if new else None, Z):
                     if t is not None:
                         t[T:].zero_()
-        st = (stream or torch.cuda.current_stream(X.device)).cuda_stream
-        plora_forward_epilogue(self.h, X.data_ptr(), W.data_ptr(), Y.data_ptr(), n, off, tab, saved.data_ptr(), ep, st)
-        if not want_Z and stream is not None:     # scratch that goes back to the allocator while the stream may use it
-            saved.record_stream(stream)
+        plora_forward_epilogue(self.h, X.data_ptr(), W.data_ptr(), Y.data_ptr(), n, off, tab, saved.data_ptr(), ep, st.cuda_stream)
+        if other is not None:      # (they may go back to the allocator while that stream uses them)
+            for t in (Y if new else None, saved if own else None, Z):
+                if t is not None:
+                    t.record_stream(other)
         return Y, saved if want_Z else None, Z
 
     def backward_epilogue(self, X, W, dY, off, scales, A, B, saved, Z=None, activation="none", want_dX=True,
@@ -663,6 +682,10 @@ class PackedLoRA:
         dX = self._gradients(X, W, dY, off, scales, A, B, saved, Z, activation, want_dX, [g.data_ptr() for g in dA],
                              [g.data_ptr() for g in dB],
                              None if db is None else [b.data_ptr() if b is not None else None for b in db], stream)
+        other = self._launch_stream(stream, X.device)[1]
+        if other is not None:
+            for t in [*dA, *dB, *(b for b in db or [] if b is not None)]:
+                t.record_stream(other)
         return dX, dA, dB, db
 
     def _gradients(self, X, W, dY, off, scales, A, B, saved, Z, activation, want_dX, pA, pB, pb, stream=None):
@@ -670,19 +693,21 @@ class PackedLoRA:
         import torch
         n = len(off) - 1
         dX = torch.empty_like(X) if want_dX else None
-        if want_dX and self._tokens(X, off) < X.shape[0]:
-            with torch.cuda.stream(stream):
-                dX[int(off[-1]):].zero_()
         tab = make_table([b.shape[1] for b in B], scales, [a.data_ptr() for a in A], [b.data_ptr() for b in B], pA, pB)
         ep = make_epilogue(activation, dbias=pb, Z=Z.data_ptr() if Z is not None else None)
         nbytes = plora_epilogue_work_bytes(self.h, n, off, ep)
         work = torch.empty(nbytes, dtype=torch.uint8, device=X.device) if nbytes else None
         ep.work = work.data_ptr() if work is not None else None
-        st = (stream or torch.cuda.current_stream(X.device)).cuda_stream
+        st, other = self._launch_stream(stream, X.device)
+        if want_dX and self._tokens(X, off) < X.shape[0]:
+            with torch.cuda.stream(st):
+                dX[int(off[-1]):].zero_()
         plora_backward_epilogue(self.h, X.data_ptr(), W.data_ptr(), dY.data_ptr(), dX.data_ptr() if want_dX else None,
-                                n, off, tab, saved.data_ptr(), ep, st)
-        if work is not None and stream is not None:
-            work.record_stream(stream)
+                                n, off, tab, saved.data_ptr(), ep, st.cuda_stream)
+        if other is not None:
+            for t in (dX, work):
+                if t is not None:
+                    t.record_stream(other)
         return dX
 
 
