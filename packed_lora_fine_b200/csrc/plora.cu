@@ -1528,6 +1528,7 @@ template <int NT> void few_launch(plora_ctx* h, const FewArgs& a, int tiles, cud
 }
 plora_status few_forward(plora_ctx* h, const void* X, const void* W, void* Y, const HostPlan& P, void* saved,
                          const EpiTables& ep, cudaStream_t st) {
+    h->in_capture = stream_capturing(st);   // (no slot is taken, which would have noted it)
     FewArgs a{};
     a.X = static_cast<const __nv_bfloat16*>(X);
     a.W = static_cast<const __nv_bfloat16*>(W);
