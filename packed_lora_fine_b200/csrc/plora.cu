@@ -1240,7 +1240,7 @@ void epilogue_grad(plora_ctx* h, const HostPlan& P, const DevPlan& D, const EpiT
 // The fp32 path's epilogue, in place on Y.
 template <typename T>
 void epilogue_apply(plora_ctx* h, const HostPlan& P, const DevPlan& D, const EpiTables& ep, void* Y, cudaStream_t st) {
-    EpiArgs a{ep.act, P.n, h->cfg.d_out, D.tok, D.bias, ep.residual, Y, ep.Z};
+    EpiArgs a{ep.act, 0, h->cfg.d_out, D.tok, D.bias, ep.residual, Y, ep.Z};
     const int64_t tiles = (int64_t)P.tok.size();
     for (int64_t t0 = 0; t0 < tiles; t0 += 65535) {
         a.tok = D.tok + t0;
@@ -2183,14 +2183,18 @@ plora_status plora_saved_bytes(plora_handle h, int32_t n, const int64_t* off, co
 
 plora_status plora_epilogue_saved_bytes(plora_handle h, int32_t n, const int64_t* off, const plora_adapter* tab,
                                         const plora_epilogue* ep, size_t* bytes) {
-    const plora_status s = plora_saved_bytes(h, n, off, tab, bytes);
-    if (s != PLORA_OK) return s;
-    if (!ep || ep->activation < PLORA_ACT_NONE || ep->activation > PLORA_ACT_SILU)
-        return fail(h, PLORA_ERR_INVALID_ARG, "no epilogue, or activation out of range");
-    HostPlan P;
-    build_plan(h, n, off, tab, P);
-    if (P.T > 0 && relu_low(h, ep->activation, ep->Z != nullptr)) *bytes = low_bytes_of(h, P);
-    return PLORA_OK;
+    try {
+        const plora_status s = plora_saved_bytes(h, n, off, tab, bytes);
+        if (s != PLORA_OK) return s;
+        if (!ep || ep->activation < PLORA_ACT_NONE || ep->activation > PLORA_ACT_SILU)
+            return fail(h, PLORA_ERR_INVALID_ARG, "no epilogue, or activation out of range");
+        HostPlan P;
+        build_plan(h, n, off, tab, P);
+        if (P.T > 0 && relu_low(h, ep->activation, ep->Z != nullptr)) *bytes = low_bytes_of(h, P);
+        return PLORA_OK;
+    } catch (const std::bad_alloc&) {
+        return fail(h, PLORA_ERR_OOM, "out of host memory");
+    }
 }
 
 plora_status plora_forward(plora_handle h, const void* X, const void* W, void* Y, int32_t n, const int64_t* off,
