@@ -414,7 +414,8 @@ PLORA_API plora_status plora_muon_step(plora_handle h, int32_t n_adapters, const
 
 /*
  * CUDA graph capture (a runtime facility; the pages describe no API).  A plora_forward,
- * plora_backward or plora_adamw_step called while its stream is being captured
+ * plora_backward, plora_forward_epilogue (but an inference call of few tokens, which takes none),
+ * plora_backward_epilogue, plora_adamw_step or plora_muon_step called while its stream is being captured
  * (cudaStreamBeginCapture, torch.cuda.graph) takes one schedule slot reserved here instead
  * of the handle's ring, and keeps it: every replay of the graph re-copies that call's
  * schedule from the slot, which no later call overwrites.  Reserve before the capture begins

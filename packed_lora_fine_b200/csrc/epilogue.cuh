@@ -22,8 +22,10 @@ constexpr float kSqrt2OverPi = 0.79788456080286536f;
 constexpr float kGeluCubic = 0.044715f;
 
 // act(z) and act'(z) for results of type T.  fp32 uses CUDA's accurate functions.  bf16 results keep 9 of 24
-// bits, so theirs use the fast exponential and division (relative errors near 2^-21) and no branch, whose 64
-// divisions per thread and chunk would otherwise run one after another:
+// bits, so theirs use the fast exponential and division and no branch, whose 64
+// divisions per thread and chunk would otherwise run one after another.  The exponential is off by 2 + 1.16 |x| units
+// of its last place: a tail's relative error grows with |z|, but what a function is off by stays below 2^-21 of |z|
+// (2^-19 for the derivatives, absolute):
 //   tanh form: (1 + tanh y) / 2 = 1 / (1 + exp(-2 y))
 //   erf form:  Abramowitz and Stegun 7.1.26, erfc(x) = t (a1 + ... + a5 t^4) exp(-x^2), t = 1 / (1 + p x), x >= 0,
 //              absolute error 1.5e-7, and exp(-z^2/2) serves the derivative as well
@@ -163,7 +165,7 @@ constexpr int kEpiCols = 256;   // columns of one block of the elementwise kerne
 
 struct EpiArgs {
     int32_t act;
-    int32_t n_adapters;
+    int32_t pad_;
     int64_t d_out;
     const TokTile* tok;          // 128-row tiles of the adapters' tokens
     const void* const* bias;     // [n] device pointers (entries may be null), or null
