@@ -512,6 +512,8 @@ class PackedLoRA:
                               max_adapters, max_rank, max_tokens,
                               (PLORA_FLAG_SIMT if simt else 0) | (PLORA_FLAG_UNFUSED if unfused else 0)
                               | (PLORA_FLAG_BASE_PAIR if base_pair else 0), out_blocks)
+        import torch
+        self.device = torch.device("cuda", torch.cuda.current_device())    # where plora_create put the handle
 
     def close(self):
         if self.h:
@@ -570,9 +572,9 @@ class PackedLoRA:
             if t is None:
                 continue
             want = shape.get(name, (T, self.d_out))
-            if t.shape != want or t.dtype != dt or not t.is_contiguous():
-                raise ValueError(f"{name}: a contiguous {dt} tensor of shape {want} is needed, got {t.dtype} "
-                                 f"{tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous'}")
+            if t.shape != want or t.dtype != dt or not t.is_contiguous() or t.device != self.device:
+                raise ValueError(f"{name}: a contiguous {dt} tensor of shape {want} on {self.device} is needed, got {t.dtype} "
+                                 f"{tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
     @staticmethod
     def _tokens(X, off) -> int:
@@ -606,9 +608,11 @@ class PackedLoRA:
         for i, (a, b) in enumerate(zip(A, B)):
             r = b.shape[1]
             if a.shape != (P * r, self.d_in) or b.shape != (self.d_out, r) or a.dtype != dt \
-                    or b.dtype != dt or not a.is_contiguous() or not b.is_contiguous():
+                    or b.dtype != dt or not a.is_contiguous() or not b.is_contiguous() \
+                    or a.device != self.device or b.device != self.device:
                 raise ValueError(f"adapter {i}: contiguous {dt} factors A {(P * r, self.d_in)} and B "
-                                 f"{(self.d_out, r)} are needed, got {tuple(a.shape)} and {tuple(b.shape)}")
+                                 f"{(self.d_out, r)} on {self.device} are needed, got {tuple(a.shape)} on {a.device} and "
+                                 f"{tuple(b.shape)} on {b.device}")
 
     def _bias_list(self, bias, n):
         """One bias (or None) per adapter from None, one tensor for every adapter, or a list."""
