@@ -588,13 +588,14 @@ class PackedLoRA:
     def _launch_stream(stream, device):
         """The stream of a call, and the same if it is not the current one, else None.  A call's new tensors come from the
         current stream's memory, where work on what was there before may not have ended: another stream waits for it
-        (one that is being captured cannot: its capture holds what it needs)."""
+        (not while either is captured: a capture holds the memory that it needs, and waits for nothing outside)."""
         import torch
         current = torch.cuda.current_stream(device)
         if stream is None or stream == current:
             return current, None
+        captured = torch.cuda.is_current_stream_capturing()
         with torch.cuda.stream(stream):
-            if torch.cuda.is_current_stream_capturing():
+            if captured or torch.cuda.is_current_stream_capturing():
                 return stream, None
         stream.wait_stream(current)
         return stream, stream
