@@ -179,6 +179,9 @@ def _prepare_muon(case, seed):
     if own:
         import packed_lora_fine_b200 as pl
         n, di, do, blocks, ranks = case["n"], case["d_in"], case["d_out"], case["blocks"], _ranks(case)
+        if case["dtype"] == "fp32" and blocks > 1:
+            # the library's output blocks are bf16's; in fp32 each block's A and B are an adapter's of their own
+            n, do, blocks, ranks = n * blocks, do // blocks, 1, [r for r in ranks for _ in range(blocks)]
         eng = pl.PackedLoRA(di, do, case["dtype"], max_adapters=n, max_rank=max(ranks), max_tokens=16,
                             out_blocks=[do // blocks] * blocks if blocks > 1 else None)
         sizes = [r * blocks * di for r in ranks] + [do * r for r in ranks]
@@ -196,7 +199,7 @@ def _prepare_muon(case, seed):
         master = case["dtype"] == "bf16"
         st = pl.make_muon_states(hp, pa if master else None, pb if master else None, ma, mb)
         work = torch.empty(pl.plora_muon_work_bytes(eng.h, n, tab), dtype=torch.uint8, device="cuda")
-        s |= {"engine": eng, "tab": tab, "states": st, "work": work}
+        s |= {"engine": eng, "adapters": n, "tab": tab, "states": st, "work": work}
     return s
 
 
@@ -306,7 +309,7 @@ def _own_layer(s):
 
 def _own_muon(s):
     import packed_lora_fine_b200 as pl
-    pl.plora_muon_step(s["engine"].h, s["case"]["n"], s["tab"], s["states"], s["work"].data_ptr(),
+    pl.plora_muon_step(s["engine"].h, s["adapters"], s["tab"], s["states"], s["work"].data_ptr(),
                        torch.cuda.current_stream().cuda_stream)
     return {"p": s["p"], "m": s["m"]} | ({"out": s["out"]} if s["out"] is not None else {})
 
