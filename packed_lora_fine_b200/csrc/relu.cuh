@@ -15,9 +15,9 @@
 //       from A too, eight products at a time in fp32 and their sums in fp64;
 //   that < 2^-20 of the first sum
 //       all in fp64.
-// with e = 1.25 2^-24 ((d_in + 2 P rblk) / 16 + 16), 1.5 times the largest drift seen and 8 times its rms, |h| the norm of the row's H' and |A|
-// Frobenius's.  (A row or column whose norm leaves fp32's range, entries past 10^18 or all below 10^-22, is left alone.)  The norms are kept
-// behind the low parts in `saved`.
+// with e = 1.25 2^-24 ((d_in + 2 P rblk) / 16 + 16), 1.5 times the largest drift seen and 8 times its rms, |h| the
+// norm of the row's H' and |A| Frobenius's.  (A row or column whose norm leaves fp32's range, entries past 10^18 or
+// all below 10^-22, is left alone.)  The norms are kept behind the low parts in `saved`.
 #pragma once
 #include <cuda_bf16.h>
 #include "epilogue.cuh"
